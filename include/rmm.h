@@ -27,7 +27,9 @@
  *   - All work is enqueued on `stream` in order; no call synchronises the
  *     host except rmm_check.
  *   - A call makes the stream's device current while it runs and restores the
- *     caller's current device before it returns.
+ *     caller's current device before it returns. While the stream is being
+ *     captured into a graph its device cannot be looked up and must already be
+ *     the current one.
  *   - Argument errors are detected on the host, before any launch, and
  *     returned as RMM_ERR_INVALID / RMM_ERR_UNSUPPORTED. A failed CUDA
  *     runtime call returns RMM_ERR_CUDA. rmm_last_error_string() describes
@@ -51,7 +53,8 @@ extern "C" {
 
 typedef enum {
   RMM_OK = 0,
-  RMM_ERR_INVALID = 1,     /* bad argument (null pointer, rho outside (0,1], bad ld, small workspace) */
+  RMM_ERR_INVALID = 1,     /* bad argument (null pointer, rho outside (0,1], bad ld, small workspace); from rmm_check:
+                              RMM_STATUS_BIT_RANGE */
   RMM_ERR_NONFINITE = 2,   /* a slice score was NaN or Inf (reported by rmm_check) */
   RMM_ERR_CUDA = 3,        /* a CUDA runtime call failed */
   RMM_ERR_TIMEOUT = 4,     /* a bounded pipeline wait in a kernel gave up (reported by rmm_check) */
@@ -65,6 +68,7 @@ typedef enum { RMM_SCORE_PRODUCT = 0, RMM_SCORE_A_ONLY = 1 } rmm_score_mode;
 /* Device status-word bits (see rmm_check). */
 #define RMM_STATUS_BIT_NONFINITE 0x1u
 #define RMM_STATUS_BIT_TIMEOUT   0x2u
+#define RMM_STATUS_BIT_RANGE     0x4u  /* a token's slot lay outside its cache (rmm_kv4_store) */
 
 /* ---------------------------------------------------------------- host helpers */
 
@@ -448,6 +452,124 @@ rmm_status rmm_matmul_reduced_noalloc(const void* A, int64_t lda, const void* B,
                                       rmm_dtype in, rmm_score_mode mode,
                                       void* C, int64_t ldc, rmm_dtype out, int32_t* idx_out,
                                       uint32_t* status_word, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- attention
+ * The attention sites of "Escopo de Aplicação" for serving: whole prompts
+ * without P in memory, the weight each key received (the key score of P·V with
+ * the plain sum in place of the norm, over all queries so far), a cache of
+ * keys and values in 4 bits with its decode step, and eviction of the cached
+ * tokens of least weight. The pages name none of these steps.
+ *
+ * Tokens are [tokens][heads][d], d contiguous, with a token stride (ts) and a
+ * head stride (hs) in elements. Query head h reads key head h / (h_q / h_kv).
+ * Packed sequences: sequence i's tokens are [cu[i], cu[i+1]), cu a device
+ * array of n_seq + 1 ascending int32; NULL for a single sequence of all
+ * tokens. Boundaries are clamped to the token count on the device; tokens of
+ * no sequence are neither read as keys nor written. */
+
+/* O = softmax(scale·Q·Kᵀ)·V per sequence and head.
+ *   Q [T_q][h_q][d], K, V [T_k][h_kv][d], O [T_q][h_q][d]: 16-byte aligned,
+ *   strides multiples of 8 elements; in must be RMM_BF16, d a multiple of 8 up
+ *   to 128, at most 128 query heads per key head (RMM_ERR_UNSUPPORTED
+ *   otherwise). Sequence i has S_q = cu_q[i+1] - cu_q[i] queries and S_k keys;
+ *   with causal != 0 query q sees key k only when k <= q + S_k - S_q (the last
+ *   query sees every key). A query that sees no key gets O = 0 and lse = -inf.
+ *   lse: nullable f32 [h_q][T_q], ln sum_k exp(scale·q·k) over the visible keys.
+ *   P is rounded to bf16 for the product with V (f32 sums; the row sum in lse
+ *   and the division takes the unrounded values), also when out is RMM_F32.
+ *   Keys and values of a sequence's own tokens must be finite, masked ones
+ *   included; memory outside the sequences may hold anything. status_word
+ *   (nullable) receives RMM_STATUS_BIT_NONFINITE when a row's sum is not a
+ *   positive finite number, RMM_STATUS_BIT_TIMEOUT as in rmm_gemm. */
+rmm_status rmm_attn_prompt(const void* Q, int64_t q_ts, int64_t q_hs, const void* K, int64_t k_ts, int64_t k_hs,
+                           const void* V, int64_t v_ts, int64_t v_hs, const int32_t* cu_q, const int32_t* cu_k,
+                           int64_t n_seq, int64_t T_q, int64_t T_k, int64_t h_q, int64_t h_kv, int64_t d, float scale,
+                           int causal, rmm_dtype in, void* O, int64_t o_ts, int64_t o_hs, rmm_dtype out, float* lse,
+                           uint32_t* status_word, cudaStream_t stream);
+
+/* The weight each key received: w_out[h][k] = w_in[h][k] + sum of
+ * exp(scale·q·k - lse[hq][q]) over the queries q that see key k and the query
+ * heads hq that read key head h. lse as rmm_attn_prompt writes it for the same
+ * arguments (which are as there). w_in, w_out: f32 [h_kv][T_k]; w_in NULL
+ * counts as zeros and may be w_out. Sums in f32 in a fixed order. */
+rmm_status rmm_attn_key_weights(const void* Q, int64_t q_ts, int64_t q_hs, const void* K, int64_t k_ts, int64_t k_hs,
+                                const int32_t* cu_q, const int32_t* cu_k, int64_t n_seq, int64_t T_q, int64_t T_k,
+                                int64_t h_q, int64_t h_kv, int64_t d, float scale, int causal, rmm_dtype in,
+                                const float* lse, const float* w_in, float* w_out, uint32_t* status_word,
+                                cudaStream_t stream);
+
+/* A cache in 4 bits. A row (one token of one head) of d channels (32, 64, 96
+ * or 128) is cut into groups of 32. A group holds a bf16 minimum m, a bf16
+ * step s = bf16((max - min) / 15) and per channel a code c =
+ * clamp(rint((x - m) / s), 0, 15) (0 where s is 0), and stands for m + s·c.
+ * Four planes, contiguous and 16-byte aligned, with room for cap tokens:
+ *   kc, vc  [batch][h_kv][cap][d/2] bytes of codes
+ *   ks, vs  [batch][h_kv][cap][d/32][2] bf16: step, minimum
+ * Within a row, with ng = d/32 and nibble i at bits 4i: kc holds 32-bit words
+ * [4][ng], word (j, g) nibble i = channel 32g + 8j + i; vc holds 16-bit words
+ * [8][ng], word (r, g) nibble i = channel 32g + 8i + r (the layouts the decode
+ * step's tensor-core operands are built from without a transposition). */
+
+/* Quantise tokens into their slots: token t of sequence b goes to slot
+ * start[b] + (t - cu[b]) of sequence b's rows; cu NULL means one token per
+ * sequence (T == n_seq). K, V [T][h_kv][d] of dtype in (bf16 or f32; any
+ * strides). w (nullable, [n_seq][h_kv][cap] f32): the slots' running weights,
+ * set to w_new[h][t] (f32 [h_kv][T]) or, w_new NULL, to 0. Tokens whose slot
+ * is outside [0, cap) are left out and set RMM_STATUS_BIT_RANGE; a NaN or Inf
+ * sets RMM_STATUS_BIT_NONFINITE (its group's contents are then unspecified).
+ * Slots must not repeat within a call. */
+rmm_status rmm_kv4_store(const void* K, int64_t k_ts, int64_t k_hs, const void* V, int64_t v_ts, int64_t v_hs,
+                         rmm_dtype in, const int32_t* cu, const int32_t* start, int64_t n_seq, int64_t T, int64_t h_kv,
+                         int64_t d, int64_t cap, uint8_t* kc, void* ks, uint8_t* vc, void* vs, const float* w_new,
+                         float* w, uint32_t* status_word, cudaStream_t stream);
+
+/* Bytes of workspace rmm_kv4_attn needs (weights: w_out is given). */
+size_t rmm_kv4_attn_workspace_size(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, int weights);
+
+/* One decode step: O[b] = softmax(scale·q·Kᵀ)·V over the first lens[b] cached
+ * tokens of sequence b (device int32, clamped to [0, cap]), one query token
+ * per sequence. Q, O [batch][h_q][d] with sequence and head strides (16-byte
+ * aligned, multiples of 8 elements), in = RMM_BF16. A sequence of no tokens
+ * gets O = 0 and lse = -inf. lse: nullable f32 [batch][h_q]. w_out (nullable,
+ * f32 [batch][h_kv][cap]): w_out[b][h][t] = w_in[b][h][t] + the probabilities
+ * of token t summed over the query heads that read head h, for t < lens[b]; w_in
+ * NULL counts as zeros and may be w_out. The probabilities (times the values'
+ * steps) are rounded to bf16 for the product, sums are f32 in a fixed order.
+ * Workspace 1 KiB-aligned, its first word the status word (rmm_check), cleared
+ * at the start. Slots at and past lens[b] are not used. */
+rmm_status rmm_kv4_attn(const void* Q, int64_t q_ss, int64_t q_hs, const uint8_t* kc, const void* ks,
+                        const uint8_t* vc, const void* vs, const int32_t* lens, int64_t batch, int64_t h_q,
+                        int64_t h_kv, int64_t d, int64_t cap, float scale, rmm_dtype in, void* O, int64_t o_ss,
+                        int64_t o_hs, rmm_dtype out, float* lse, const float* w_in, float* w_out, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+
+/* A plane of cached rows: src [batch][heads][cap] and dst
+ * [batch][heads][cap_out] rows of row_bytes (a multiple of 4, up to 8192)
+ * bytes, contiguous, 4-byte aligned (16-byte aligned rows move fastest). dst
+ * may be src (with cap_out == cap): the rows are then moved in place. Apart
+ * from that no plane may overlap another. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t row_bytes;
+} rmm_cache_plane;
+
+size_t rmm_cache_evict_workspace_size(int64_t batch, int64_t heads, int64_t budget);
+
+/* Keep at most `budget` of each (sequence, head)'s lens[b] cached tokens: the
+ * first `sink`, the last `recent` (sink + recent <= budget) and of the others
+ * those of greatest w (f32 [batch][heads][cap]; ties to the lower index), all
+ * in their order; with lens[b] <= budget, all of them. The kept rows of every
+ * plane (at most 8; w itself may be one) move to the front of its dst; rows of
+ * dst past them are left as they are. lens_out[b] = min(lens[b], budget) (may
+ * be lens); idx_out (nullable, i32 [batch][heads][budget]): the kept tokens'
+ * former indices, ascending, -1 past them. A NaN or infinite weight among the
+ * candidates sets RMM_STATUS_BIT_NONFINITE. The workspace's first word is the
+ * status word, cleared at the start. */
+rmm_status rmm_cache_evict(const float* w, const int32_t* lens, int64_t batch, int64_t heads, int64_t cap,
+                           int64_t budget, int64_t sink, int64_t recent, const rmm_cache_plane* planes,
+                           int64_t n_planes, int64_t cap_out, int32_t* lens_out, int32_t* idx_out, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------- diagnostics */
 

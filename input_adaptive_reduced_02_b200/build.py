@@ -20,8 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librmm.so")
 SOURCES = ["api.cu", "score.cu", "select.cu", "pack.cu", "gemm_tc.cu", "gemm_simt.cu", "gemv.cu", "softmax.cu",
-           "noalloc.cu"]
-HEADERS = ["rmm_device.cuh", "rmm_internal.h", "int8_convert.cuh"]
+           "noalloc.cu", "attn.cu", "kv4.cu", "evict.cu", "api_attn.cu"]
+HEADERS = ["rmm_device.cuh", "rmm_internal.h", "int8_convert.cuh", "api_common.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

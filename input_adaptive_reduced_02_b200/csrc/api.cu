@@ -12,22 +12,9 @@
 #include <cstdio>
 #include <cstring>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "../../include/rmm.h"
-#include "rmm_internal.h"
+#include "api_common.h"
 
 namespace rmm {
-
-// A named NVTX range around one stage of a call, so that a profiler's
-// timeline (or an ncu --nvtx filter) shows score, select, pack and the product
-// by name; header-only NVTX costs a branch when no tool is attached.
-struct StageRange {
-  explicit StageRange(const char* name) { nvtxRangePushA(name); }
-  ~StageRange() { nvtxRangePop(); }
-  StageRange(const StageRange&) = delete;
-  StageRange& operator=(const StageRange&) = delete;
-};
 
 static std::atomic<uint64_t> g_launches{0};
 static std::atomic<uint64_t> g_wait_limit_ns{0};
@@ -40,7 +27,7 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 static thread_local char g_err[512] = "";
 
-static rmm_status fail(rmm_status s, const char* fmt, ...) {
+rmm_status fail(rmm_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);
@@ -50,7 +37,7 @@ static rmm_status fail(rmm_status s, const char* fmt, ...) {
 
 void set_last_error(const char* msg) { snprintf(g_err, sizeof(g_err), "%s", msg); }
 
-static rmm_status cuda_fail(cudaError_t e, const char* what, const char* why = nullptr) {
+rmm_status cuda_fail(cudaError_t e, const char* what, const char* why) {
   return fail(RMM_ERR_CUDA, "%s: %s%s%s", what, cudaGetErrorString(e), why ? " — " : "", why ? why : "");
 }
 
@@ -62,7 +49,7 @@ static rmm_status cuda_fail(cudaError_t e, const char* what, const char* why = n
 // device status word; both synchronise the stream.
 static std::atomic<int> g_debug{-1};  // -1: not yet read from the environment
 
-static bool debug_on() {
+bool debug_on() {
   int d = g_debug.load();
   if (d < 0) {
     const char* e = std::getenv("RMM_DEBUG");
@@ -112,21 +99,23 @@ static rmm_status debug_check_indices(const int32_t* idx, int64_t batch, int64_t
               (long long)K, (long long)(got[1] / k_keep), (long long)(got[1] % k_keep), v);
 }
 
-// Debug mode, after a fused call: wait for it and return its device status.
-static rmm_status debug_call_status(uint32_t* status, cudaStream_t st) {
+rmm_status status_error(uint32_t w) {
+  if (w & RMM_STATUS_BIT_TIMEOUT) return fail(RMM_ERR_TIMEOUT, "a pipeline wait in a tensor-core kernel ran out");
+  if (w & RMM_STATUS_BIT_RANGE) return fail(RMM_ERR_INVALID, "a token's slot lay outside the cache");
+  if (w & RMM_STATUS_BIT_NONFINITE)
+    return fail(RMM_ERR_NONFINITE, "a slice score, an attention row or a cached value was NaN or Inf");
+  return RMM_OK;
+}
+
+rmm_status debug_call_status(uint32_t* status, cudaStream_t st) {
   uint32_t w = 0;
   cudaError_t e = cudaMemcpyAsync(&w, status, sizeof(w), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "reading the status word (debug)");
-  if (w & RMM_STATUS_BIT_TIMEOUT) return fail(RMM_ERR_TIMEOUT, "a pipeline wait in the GEMM ran out");
-  if (w & RMM_STATUS_BIT_NONFINITE) return fail(RMM_ERR_NONFINITE, "a slice score was NaN or Inf");
-  return RMM_OK;
+  return status_error(w);
 }
 
-// Make the stream's device current for the rest of the call (the caller's
-// framework may have made another device current); `g` puts the caller's
-// device back when the entry point returns.
-static rmm_status bind_device(cudaStream_t st, DeviceGuard& g) {
+rmm_status bind_device(cudaStream_t st, DeviceGuard& g) {
   const cudaError_t e = g.bind(st);
   if (e != cudaSuccess) return cuda_fail(e, "selecting the stream's device");
   return RMM_OK;
@@ -137,13 +126,10 @@ static inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * 
 // Row pitch (elements) of the packed N-major B operand.
 static inline int64_t packed_b_ld(int64_t N) { return round_up(N, 8); }
 
-static uint64_t wait_limit() {
+uint64_t wait_limit() {
   const uint64_t lim = g_wait_limit_ns.load();
   return lim ? lim : kDefaultWaitLimitNs;
 }
-
-static bool dtype_ok(rmm_dtype d) { return d == RMM_BF16 || d == RMM_F32; }
-static ElemKind kind(rmm_dtype d) { return d == RMM_BF16 ? kBF16 : kF32; }
 
 // A batch of row-major matrices (rows x cols, leading dimension ld, batch
 // stride bstride) must fit its own declared layout.
@@ -158,9 +144,6 @@ static bool layout_ok(int64_t batch, int64_t rows, int64_t cols, int64_t ld, int
 }
 
 constexpr int64_t kMaxGridBatch = 65535;
-// Slices per selection: the select kernel indexes keys with 32-bit integers
-// and re-reads them from global memory beyond 32768; 2^21 bounds its work.
-constexpr int64_t kMaxSelectK = int64_t(1) << 21;
 
 struct Workspace {
   uint32_t* status;
@@ -773,9 +756,7 @@ rmm_status rmm_check(void* status_word, cudaStream_t stream) {
   if (ce == cudaSuccess) ce = cudaMemsetAsync(status_word, 0, 4, stream);
   if (ce == cudaSuccess) ce = cudaStreamSynchronize(stream);
   if (ce != cudaSuccess) return cuda_fail(ce, "rmm_check");
-  if (w & RMM_STATUS_BIT_TIMEOUT) return fail(RMM_ERR_TIMEOUT, "a pipeline wait in the GEMM ran out");
-  if (w & RMM_STATUS_BIT_NONFINITE) return fail(RMM_ERR_NONFINITE, "a slice score was NaN or Inf");
-  return RMM_OK;
+  return status_error(w);
 }
 
 const char* rmm_last_error_string(void) { return g_err; }

@@ -14,6 +14,7 @@ namespace rmm {
 // Status-word bits, as published in rmm.h.
 constexpr uint32_t RMM_NONFINITE_BIT = 0x1u;
 constexpr uint32_t RMM_TIMEOUT_BIT = 0x2u;
+constexpr uint32_t RMM_RANGE_BIT = 0x4u;
 
 // ---------------------------------------------------------------- conversions
 // bf16 -> f32 is exact: the bf16 word is the upper half of the f32 word.

@@ -30,7 +30,13 @@ struct DeviceGuard {
   DeviceGuard(const DeviceGuard&) = delete;
   DeviceGuard& operator=(const DeviceGuard&) = delete;
   // Returns the CUDA error of the lookup or switch (cudaSuccess on success).
+  // A stream that is being captured may not be asked for its device (the
+  // question ends the capture): the current device is then left as it is, and
+  // a launch on another device's stream fails by itself.
   cudaError_t bind(cudaStream_t st) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) cudaGetLastError();
+    if (capture == cudaStreamCaptureStatusActive) return cudaSuccess;
     int dev = -1;
     cudaError_t e = cudaStreamGetDevice(st, &dev);
     if (e != cudaSuccess) return e;
@@ -79,6 +85,10 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 }
 // Sets the message rmm_last_error_string() returns on the calling thread.
 void set_last_error(const char* msg);
+// The limit of a kernel's bounded waits (rmm_set_wait_limit_ns) and whether
+// debug checks are on (rmm_set_debug).
+uint64_t wait_limit();
+bool debug_on();
 
 // score.cu
 //  s[b][k] = sqrt(sum_i A[b][i][k]^2) · (bmode 1: sqrt(sum_j B[b][k][j]^2) with B
@@ -233,5 +243,100 @@ cudaError_t launch_gemv_gather(const GemvArgs& g, cudaStream_t st);
 //  B = an INT8 weight (g.b int8, rows 4-byte aligned) whose column j is scaled
 //  by scale[b * s_stride + j]; A bf16.
 cudaError_t launch_gemv_gather_w8(const GemvArgs& g, const float* scale, int64_t s_stride, cudaStream_t st);
+
+// ---------------------------------------------------------------- attention
+// Tokens of packed sequences, [tokens][heads][d] with strides in elements.
+struct TokView {
+  const void* ptr;
+  int64_t ts, hs;  // token and head stride
+};
+
+// attn.cu: sequence i's queries are tokens [cu_q[i], cu_q[i+1]) and its keys
+// [cu_k[i], cu_k[i+1]) (cu null: one sequence of all tokens); the boundaries
+// are clamped to [0, T] on the device. Causal: key k is visible to query q
+// when k <= q + S_k - S_q.
+struct AttnArgs {
+  TokView q, k, v;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t n_seq, T_q, T_k, h_q, h_kv, d;
+  float scale;
+  int causal;
+  void* o;  // [T_q][h_q][d] at o_ts / o_hs
+  int64_t o_ts, o_hs;
+  ElemKind out;
+  float* lse;         // [h_q][T_q], nullable for the attention itself
+  const float* w_in;  // [h_kv][T_k], nullable; key weights only
+  float* w_out;       // [h_kv][T_k]
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_attn_prompt(const AttnArgs& a, cudaStream_t st, const char** why);
+cudaError_t launch_attn_key_weights(const AttnArgs& a, cudaStream_t st, const char** why);
+
+// kv4.cu: a cache of keys and values in 4 bits.
+constexpr int64_t kKv4Group = 32;   // channels per scale and minimum
+constexpr int64_t kKv4MaxD = 128;
+struct Kv4Planes {
+  uint8_t* kc;   // codes [batch][h_kv][cap][d/2]
+  uint16_t* ks;  // bf16 (step, minimum) [batch][h_kv][cap][d/32][2]
+  uint8_t* vc;
+  uint16_t* vs;
+};
+struct Kv4StoreArgs {
+  TokView k, v;
+  ElemKind in;
+  const int32_t* cu;     // [n_seq + 1] or null: token b is sequence b's only one
+  const int32_t* start;  // [n_seq] slot of each sequence's first token
+  int64_t n_seq, T, h_kv, d, cap;
+  Kv4Planes c;
+  const float* w_new;  // [h_kv][T], nullable (zeros)
+  float* w;            // [n_seq][h_kv][cap], nullable
+  uint32_t* status;
+};
+cudaError_t launch_kv4_store(const Kv4StoreArgs& a, cudaStream_t st);
+
+// Workspace of one decode call, in bytes from its 1 KiB-aligned base.
+struct Kv4Ws {
+  int64_t split_len, max_splits;
+  size_t ml, o, scores, bytes;
+};
+Kv4Ws kv4_ws(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, bool weights);
+struct Kv4AttnArgs {
+  const void* q;  // [batch][h_q][d] bf16 at q_ss / q_hs
+  int64_t q_ss, q_hs;
+  Kv4Planes c;
+  const int32_t* lens;
+  int64_t batch, h_q, h_kv, d, cap;
+  float scale;
+  void* o;
+  int64_t o_ss, o_hs;
+  ElemKind out;
+  float* lse;  // [batch][h_q], nullable
+  const float* w_in;
+  float* w_out;  // [batch][h_kv][cap], nullable
+  void* workspace;  // status word first
+};
+cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st);
+
+// evict.cu
+constexpr int kMaxPlanes = 8;
+struct EvictPlane {
+  const void* src;
+  void* dst;
+  int64_t row_bytes;
+};
+struct EvictArgs {
+  const float* w;  // [batch][heads][cap]
+  const int32_t* lens;
+  int64_t batch, heads, cap, cap_out, budget, sink, recent;
+  EvictPlane plane[kMaxPlanes];
+  int n_planes;
+  int32_t* lens_out;
+  int32_t* idx;     // [batch][heads][budget]
+  int32_t* counts;  // [batch][heads] scratch
+  uint32_t* status;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
 
 }  // namespace rmm

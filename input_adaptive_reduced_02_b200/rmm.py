@@ -82,6 +82,16 @@ _SIGS = {
     "rmm_pv_softmax_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64, _i64, _i64]),
     "rmm_pv_softmax_reduced": (_i32, [_vp, _i32, ctypes.c_float, _i32, _vp, _i64, _i64, _i64, _i64, _f64, _i32, _vp,
                                       _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp]),
+    "rmm_attn_prompt": (_i32, [_vp, _i64, _i64] * 3 + [_vp, _vp] + [_i64] * 6 + [ctypes.c_float, _i32, _i32, _vp,
+                                                                                 _i64, _i64, _i32, _vp, _vp, _vp]),
+    "rmm_attn_key_weights": (_i32, [_vp, _i64, _i64] * 2 + [_vp, _vp] + [_i64] * 6 + [ctypes.c_float, _i32, _i32] +
+                             [_vp] * 5),
+    "rmm_kv4_store": (_i32, [_vp, _i64, _i64] * 2 + [_i32, _vp, _vp] + [_i64] * 5 + [_vp] * 8),
+    "rmm_kv4_attn_workspace_size": (ctypes.c_size_t, [_i64] * 5 + [_i32]),
+    "rmm_kv4_attn": (_i32, [_vp, _i64, _i64] + [_vp] * 5 + [_i64] * 5 + [ctypes.c_float, _i32, _vp, _i64, _i64, _i32] +
+                     [_vp] * 4 + [ctypes.c_size_t, _vp]),
+    "rmm_cache_evict_workspace_size": (ctypes.c_size_t, [_i64] * 3),
+    "rmm_cache_evict": (_i32, [_vp, _vp] + [_i64] * 6 + [_vp, _i64, _i64] + [_vp] * 3 + [ctypes.c_size_t, _vp]),
     "rmm_check": (_i32, [_vp, _vp]),
     "rmm_last_error_string": (ctypes.c_char_p, []),
     "rmm_set_wait_limit_ns": (None, [_u64]),
@@ -617,6 +627,246 @@ def pv_softmax_reduced(L: torch.Tensor, V: torch.Tensor, rho: float, scale: floa
                                         float(rho), SCORE_MODES[mode], _ptr(P), _ptr(out), _out_code(out.dtype),
                                         _ptr(idx_out), ctypes.c_void_p(ws.ptr), ws.nbytes, _stream(L)))
     return out, P, ws
+
+
+# ---------------------------------------------------------------- attention
+def _tokens(t: torch.Tensor, name: str):
+    """(tokens, heads, d, token_stride, head_stride) of a [tokens][heads][d] CUDA tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][d]")
+    n, h, d = t.shape
+    if d > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    return n, h, d, t.stride(0) if n > 1 else h * d, t.stride(1) if h > 1 else d
+
+
+def _i32_vec(t: torch.Tensor, name: str, n: int, device):
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements on {device}")
+    return t
+
+
+def _f32_shape(t: torch.Tensor | None, name: str, shape, device):
+    if t is not None and (t.dtype != torch.float32 or t.device != device or not t.is_contiguous()
+                          or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor on {device}")
+    return t
+
+
+def _packed(Q: torch.Tensor, K: torch.Tensor, cu_q, cu_k):
+    """Sizes and strides of packed queries and keys, and the number of sequences."""
+    T_q, h_q, d, q_ts, q_hs = _tokens(Q, "Q")
+    T_k, h_kv, dk, k_ts, k_hs = _tokens(K, "K")
+    if dk != d or K.device != Q.device or K.dtype != Q.dtype:
+        raise ValueError("Q and K disagree on d, dtype or device")
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k go together")
+    n = 1 if cu_q is None else cu_q.numel() - 1
+    if n < 0:
+        raise ValueError("cu_q must hold n_seq + 1 boundaries")
+    if cu_q is not None:
+        _i32_vec(cu_q, "cu_q", n + 1, Q.device)
+        _i32_vec(cu_k, "cu_k", n + 1, Q.device)
+    return T_q, T_k, h_q, h_kv, d, q_ts, q_hs, k_ts, k_hs, n
+
+
+def attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor | None = None,
+                cu_k: torch.Tensor | None = None, scale: float | None = None, causal: bool = True,
+                out_dtype=torch.float32, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                status: torch.Tensor | None = None):
+    """(O, lse): O = softmax(scale·Q·Kᵀ)·V of packed prompts, lse its rows' log-sum-exp.
+
+    Q [T_q][h_q][d], K, V [T_k][h_kv][d] bf16; sequence i's tokens are
+    [cu[i], cu[i+1]) (int32, on the device; None: one sequence). With causal,
+    query q sees key k when k <= q + S_k - S_q. scale defaults to 1/sqrt(d).
+    O [T_q][h_q][d]; lse f32 [h_q][T_q]."""
+    T_q, T_k, h_q, h_kv, d, q_ts, q_hs, k_ts, k_hs, n = _packed(Q, K, cu_q, cu_k)
+    tv, hv, dv, v_ts, v_hs = _tokens(V, "V")
+    if (tv, hv, dv) != (T_k, h_kv, d) or V.device != Q.device or V.dtype != Q.dtype:
+        raise ValueError("K and V disagree on shape, dtype or device")
+    if out is None:
+        out = torch.empty(T_q, h_q, d, dtype=out_dtype, device=Q.device)
+    elif tuple(out.shape) != (T_q, h_q, d) or out.device != Q.device:
+        raise ValueError("out must be [T_q][h_q][d] on Q's device")
+    _, _, _, o_ts, o_hs = _tokens(out, "out")
+    if lse is None:
+        lse = torch.empty(h_q, T_q, dtype=torch.float32, device=Q.device)
+    _f32_shape(lse, "lse", (h_q, T_q), Q.device)
+    _check(lib().rmm_attn_prompt(_ptr(Q), q_ts, q_hs, _ptr(K), k_ts, k_hs, _ptr(V), v_ts, v_hs, _ptr(cu_q),
+                                 _ptr(cu_k), n, T_q, T_k, h_q, h_kv, d, float(d ** -0.5 if scale is None else scale),
+                                 int(causal), _dtype(Q), _ptr(out), o_ts, o_hs, _out_code(out.dtype), _ptr(lse),
+                                 _ptr(status), _stream(Q)))
+    return out, lse
+
+
+def attn_key_weights(Q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor | None = None,
+                     cu_k: torch.Tensor | None = None, scale: float | None = None, causal: bool = True,
+                     w_in: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     status: torch.Tensor | None = None) -> torch.Tensor:
+    """[h_kv][T_k] f32: w_in (or 0) plus the attention each key received, summed
+    over its sequence's queries and over the query heads that read its head.
+    Arguments as attn_prompt's, whose lse it takes; out may be w_in."""
+    T_q, T_k, h_q, h_kv, d, q_ts, q_hs, k_ts, k_hs, n = _packed(Q, K, cu_q, cu_k)
+    _f32_shape(lse, "lse", (h_q, T_q), Q.device)
+    _f32_shape(w_in, "w_in", (h_kv, T_k), Q.device)
+    if out is None:
+        out = torch.empty(h_kv, T_k, dtype=torch.float32, device=Q.device)
+    _f32_shape(out, "out", (h_kv, T_k), Q.device)
+    _check(lib().rmm_attn_key_weights(_ptr(Q), q_ts, q_hs, _ptr(K), k_ts, k_hs, _ptr(cu_q), _ptr(cu_k), n, T_q, T_k,
+                                      h_q, h_kv, d, float(d ** -0.5 if scale is None else scale), int(causal),
+                                      _dtype(Q), _ptr(lse), _ptr(w_in), _ptr(out), _ptr(status), _stream(Q)))
+    return out
+
+
+KV4_GROUP = 32
+
+
+class KV4Cache:
+    """The planes of a cache of keys and values in 4 bits (include/rmm.h has the
+    layout): kc, vc [batch][heads][cap][d/2] uint8 codes, ks, vs
+    [batch][heads][cap][d/32][2] bf16 steps and minima, and optionally w
+    [batch][heads][cap] f32, the tokens' running attention weights."""
+
+    def __init__(self, kc: torch.Tensor, ks: torch.Tensor, vc: torch.Tensor, vs: torch.Tensor,
+                 w: torch.Tensor | None = None):
+        if kc.dim() != 4 or kc.dtype != torch.uint8 or not kc.is_cuda:
+            raise ValueError("kc must be a [batch][heads][cap][d/2] uint8 CUDA tensor")
+        self.batch, self.heads, self.cap, half = kc.shape
+        self.d = 2 * half
+        scales = (self.batch, self.heads, self.cap, self.d // KV4_GROUP, 2)
+        for name, t, dt, shape in (("kc", kc, torch.uint8, kc.shape), ("vc", vc, torch.uint8, kc.shape),
+                                   ("ks", ks, torch.bfloat16, scales), ("vs", vs, torch.bfloat16, scales)):
+            if t.dtype != dt or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != kc.device:
+                raise ValueError(f"{name} must be a contiguous {dt} {list(shape)} tensor on {kc.device}")
+        self.kc, self.ks, self.vc, self.vs = kc, ks, vc, vs
+        self.w = _f32_shape(w, "w", (self.batch, self.heads, self.cap), kc.device)
+
+    @classmethod
+    def empty(cls, batch: int, heads: int, cap: int, d: int, device="cuda", weights: bool = True) -> "KV4Cache":
+        """A cache with room for `cap` tokens per sequence (zeroed)."""
+        if d % KV4_GROUP:
+            raise ValueError(f"d must be a multiple of {KV4_GROUP}")
+        codes = lambda: torch.zeros(batch, heads, cap, d // 2, dtype=torch.uint8, device=device)  # noqa: E731
+        scales = lambda: torch.zeros(batch, heads, cap, d // KV4_GROUP, 2, dtype=torch.bfloat16,  # noqa: E731
+                                     device=device)
+        w = torch.zeros(batch, heads, cap, dtype=torch.float32, device=device) if weights else None
+        return cls(codes(), scales(), codes(), scales(), w)
+
+    def planes(self):
+        """The tensors whose rows belong to a token, for cache_evict."""
+        return [self.kc, self.ks, self.vc, self.vs] + ([self.w] if self.w is not None else [])
+
+
+def kv4_store(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, start: torch.Tensor,
+              cu: torch.Tensor | None = None, w_new: torch.Tensor | None = None,
+              status: torch.Tensor | None = None) -> KV4Cache:
+    """Quantise tokens into the cache: K, V [T][heads][d] (bf16 or f32), sequence
+    b's tokens [cu[b], cu[b+1]) going to its slots start[b], start[b] + 1, ...
+    (cu None: one token per sequence). The slots' running weights are set to
+    w_new [heads][T], or to 0."""
+    T, h, d, k_ts, k_hs = _tokens(K, "K")
+    tv, hv, dv, v_ts, v_hs = _tokens(V, "V")
+    if (tv, hv, dv) != (T, h, d) or (h, d) != (cache.heads, cache.d) or V.dtype != K.dtype:
+        raise ValueError("K, V and the cache disagree on shape or dtype")
+    if K.device != cache.kc.device or V.device != K.device:
+        raise ValueError("K, V and the cache must be on one device")
+    _i32_vec(start, "start", cache.batch, K.device)
+    if cu is not None:
+        _i32_vec(cu, "cu", cache.batch + 1, K.device)
+    _f32_shape(w_new, "w_new", (h, T), K.device)
+    _check(lib().rmm_kv4_store(_ptr(K), k_ts, k_hs, _ptr(V), v_ts, v_hs, _dtype(K), _ptr(cu), _ptr(start),
+                               cache.batch, T, h, d, cache.cap, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc),
+                               _ptr(cache.vs), _ptr(w_new), _ptr(cache.w), _ptr(status), _stream(K)))
+    return cache
+
+
+def kv4_attn_workspace_size(batch: int, h_q: int, h_kv: int, d: int, cap: int, weights: bool = False) -> int:
+    return int(lib().rmm_kv4_attn_workspace_size(batch, h_q, h_kv, d, cap, int(weights)))
+
+
+def kv4_attn(Q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, scale: float | None = None,
+             out_dtype=torch.float32, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+             w_in: torch.Tensor | None = None, w_out: torch.Tensor | None = None,
+             workspace: Workspace | None = None):
+    """(O, lse, workspace): one decode step, Q [batch][h_q][d] bf16 over the first
+    lens[b] cached tokens of each sequence. With w_out ([batch][heads][cap] f32)
+    the tokens' probabilities, summed over the query heads of their head, are
+    added to w_in (None: 0) and written to w_out, which may be w_in."""
+    n, h_q, d, q_ss, q_hs = _tokens(Q, "Q")
+    if n != cache.batch or d != cache.d or Q.device != cache.kc.device:
+        raise ValueError("Q and the cache disagree on batch, d or device")
+    _i32_vec(lens, "lens", n, Q.device)
+    for name, t in (("w_in", w_in), ("w_out", w_out)):
+        _f32_shape(t, name, (n, cache.heads, cache.cap), Q.device)
+    ws = _ensure_ws(workspace, kv4_attn_workspace_size(n, h_q, cache.heads, d, cache.cap, w_out is not None), Q.device)
+    if out is None:
+        out = torch.empty(n, h_q, d, dtype=out_dtype, device=Q.device)
+    elif tuple(out.shape) != (n, h_q, d) or out.device != Q.device:
+        raise ValueError("out must be [batch][h_q][d] on Q's device")
+    _, _, _, o_ss, o_hs = _tokens(out, "out")
+    if lse is None:
+        lse = torch.empty(n, h_q, dtype=torch.float32, device=Q.device)
+    _f32_shape(lse, "lse", (n, h_q), Q.device)
+    _check(lib().rmm_kv4_attn(_ptr(Q), q_ss, q_hs, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs),
+                              _ptr(lens), n, h_q, cache.heads, d, cache.cap,
+                              float(d ** -0.5 if scale is None else scale), _dtype(Q), _ptr(out), o_ss, o_hs,
+                              _out_code(out.dtype), _ptr(lse), _ptr(w_in), _ptr(w_out), ctypes.c_void_p(ws.ptr),
+                              ws.nbytes, _stream(Q)))
+    return out, lse, ws
+
+
+class _Plane(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
+
+
+def cache_evict_workspace_size(batch: int, heads: int, budget: int) -> int:
+    return int(lib().rmm_cache_evict_workspace_size(batch, heads, budget))
+
+
+def cache_evict(w: torch.Tensor, lens: torch.Tensor, planes, budget: int, sink: int = 0, recent: int = 0,
+                lens_out: torch.Tensor | None = None, idx_out: torch.Tensor | None = None,
+                workspace: Workspace | None = None):
+    """(lens_out, idx, workspace): keep at most `budget` cached tokens per
+    (sequence, head): the first `sink`, the last `recent`, and of the others
+    those of greatest weight w [batch][heads][cap] (ties to the lower index).
+
+    planes: the tensors [batch][heads][cap][...] whose rows move with the
+    tokens, each alone (moved in place; KV4Cache.planes()) or as a pair (src,
+    dst [batch][heads][cap_out][...]). idx [batch][heads][budget] holds the kept
+    tokens' former indices, -1 past them. lens_out may be lens."""
+    if w.dim() != 3 or w.dtype != torch.float32 or not w.is_cuda or not w.is_contiguous():
+        raise ValueError("w must be a contiguous float32 [batch][heads][cap] CUDA tensor")
+    batch, heads, cap = w.shape
+    _i32_vec(lens, "lens", batch, w.device)
+    pairs = [p if isinstance(p, tuple) else (p, p) for p in planes]
+    caps = {d.shape[2] for _, d in pairs if d.dim() >= 3}
+    if len(caps) > 1:
+        raise ValueError("the planes' destinations disagree on their capacity")
+    cap_out = caps.pop() if caps else max(cap, int(budget))
+    arr = (_Plane * max(1, len(pairs)))()
+    for i, (src, dst) in enumerate(pairs):
+        if (src.dim() < 3 or tuple(src.shape[:3]) != (batch, heads, cap) or src.dtype != dst.dtype
+                or tuple(dst.shape) != (batch, heads, cap_out, *src.shape[3:])
+                or not src.is_contiguous() or not dst.is_contiguous()
+                or src.device != w.device or dst.device != w.device):
+            raise ValueError(f"plane {i}: src and dst must be contiguous [batch][heads][cap][...] tensors like w")
+        row = src.element_size()
+        for n in src.shape[3:]:
+            row *= n
+        arr[i] = _Plane(src.data_ptr(), dst.data_ptr(), row)
+    if lens_out is None:
+        lens_out = torch.empty(batch, dtype=torch.int32, device=w.device)
+    _i32_vec(lens_out, "lens_out", batch, w.device)
+    if idx_out is None:
+        idx_out = torch.empty(batch, heads, int(budget), dtype=torch.int32, device=w.device)
+    _i32_vec(idx_out, "idx_out", batch * heads * int(budget), w.device)
+    ws = _ensure_ws(workspace, cache_evict_workspace_size(batch, heads, int(budget)), w.device)
+    _check(lib().rmm_cache_evict(_ptr(w), _ptr(lens), batch, heads, cap, int(budget), int(sink), int(recent), arr,
+                                 len(pairs), cap_out, _ptr(lens_out), _ptr(idx_out), ctypes.c_void_p(ws.ptr),
+                                 ws.nbytes, _stream(w)))
+    return lens_out, idx_out, ws
 
 
 def set_wait_limit_ns(ns: int):
