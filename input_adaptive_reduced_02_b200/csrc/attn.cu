@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "rmm_device.cuh"
 #include "rmm_internal.h"
@@ -44,6 +45,7 @@ struct TcArgs {
   AttnArgs a;
   int32_t g, nq_tile;  // heads per key head, queries per tile
   int32_t row_bytes;   // bytes of one tile's Q box: nq_tile·g·128
+  uint32_t split;      // key weights: CTAs of a cluster that share the queries
 };
 
 struct SeqSpan {
@@ -110,6 +112,28 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two f32 operations in one instruction.
+__device__ __forceinline__ uint64_t as_u64(float2 x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
+  return r;
+}
+__device__ __forceinline__ float2 as_f32x2(uint64_t r) {
+  float2 x;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(r));
+  return x;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f32x2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f32x2(r);
 }
 
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t* status) {
@@ -460,57 +484,339 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (warp == 8) tmem_dealloc<1>(tmem, 512);
 }
 
-// A thread per key of one head; the queries go by in order.
-constexpr int kMaxD = 128;
+// ---------------------------------------------------------------- key weights
+// Per CTA two tiles of 128 keys of one head: S_tᵀ = K_t·Qᵀ against tiles of 128
+// (query, head) pairs, so that a thread owns a key and sums its row of S_tᵀ
+// without leaving its registers:
+//   warps 0-3, 4-7  one key per thread: sum of 2^(s·c - lse·log2 e) over the
+//                   tile's pairs, added to the key's total with compensation
+//   warp 8          one lane issues tcgen05.mma; S_t is double buffered, so a
+//                   tile's products run while the sums of the one before do
+//   warp 9          TMA: both K tiles once, then Q tiles through a ring
+//   warp 10         -lse·log2 e of a Q tile's pairs, through a ring of its own
+// The CTAs of a cluster share the queries of the same keys, tile i going to
+// CTA i mod C, and add their sums through distributed shared memory in rank
+// order: no atomics, no workspace, one result whatever the schedule.
+constexpr int kWtThreads = 352;
+constexpr int kLseRing = 4;
 
-__device__ __forceinline__ float dot_row(const uint16_t* k, const float* q, int d) {
-  float x = 0.f;
-  for (int c = 0; c < d; c += 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(k + c);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x = fmaf(q[c + 2 * e], __uint_as_float(w[e] << 16), x);
-      x = fmaf(q[c + 2 * e + 1], __uint_as_float(w[e] & 0xFFFF0000u), x);
-    }
-  }
+template <int DP>
+struct WeightCfg {
+  static constexpr int BOXES = DP / 64;
+  static constexpr uint32_t BOX = kRows * 128;
+  static constexpr uint32_t TILE = BOXES * BOX;
+  static constexpr int STAGES = 4;
+  static constexpr uint32_t LSE = kLseRing * kRows * 4;
+  static constexpr uint32_t SUMS = 2 * kRows * 4;
+  static constexpr size_t SMEM = 1024 + size_t(2 + STAGES) * TILE + LSE + SUMS + 256;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr) : "memory");
   return x;
 }
 
-__global__ void __launch_bounds__(128) attn_key_weights_kernel(const AttnArgs a) {
-  __shared__ float qs[kMaxD];
-  pdl_trigger();
-  pdl_wait();
-  const int64_t h = blockIdx.y;
-  const int64_t i = blockIdx.z;
-  const SeqSpan s = seq_span(a, i);
-  const int d = int(a.d), g = int(a.h_q / a.h_kv);
-  const int64_t kb = int64_t(s.k0) + int64_t(blockIdx.x) * 128;
-  if (kb >= s.k1) return;
-  const int64_t k = kb + threadIdx.x;
-  const int64_t off = int64_t(s.k1 - s.k0) - (s.q1 - s.q0);
-  const uint16_t* kr = static_cast<const uint16_t*>(a.k.ptr) + h * a.k.hs + min(k, int64_t(s.k1) - 1) * a.k.ts;
-  float w = 0.f;
-  for (int64_t t = s.q0; t < s.q1; ++t) {
-    const int64_t end = a.causal ? min(int64_t(s.k1), int64_t(s.k0) + (t - s.q0) + off + 1) : int64_t(s.k1);
-    if (end <= kb) continue;
-    float part = 0.f;
-    for (int e = 0; e < g; ++e) {
-      const int64_t hq = h * g + e;
-      __syncthreads();
-      if (int(threadIdx.x) < d)
-        qs[threadIdx.x] =
-            bf16_to_f32((static_cast<const uint16_t*>(a.q.ptr) + t * a.q.ts + hq * a.q.hs)[threadIdx.x]) * a.scale;
-      __syncthreads();
-      if (k < end) part += expf(dot_row(kr, qs, d) - a.lse[hq * a.T_q + t]);
+template <int DP>
+__global__ void __launch_bounds__(kWtThreads, 1)
+attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const TcArgs p) {
+  using Cfg = WeightCfg<DP>;
+  constexpr int STAGES = Cfg::STAGES;
+  extern __shared__ uint8_t attn_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(attn_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;                 // two tiles
+  uint8_t* sQ = sK + 2 * Cfg::TILE;   // ring
+  float* lse_sh = reinterpret_cast<float*>(sQ + STAGES * Cfg::TILE);
+  float* sum_sh = lse_sh + kLseRing * kRows;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sum_sh + 2 * kRows);
+  uint64_t* empty = full + STAGES;
+  uint64_t* l_full = empty + STAGES;
+  uint64_t* l_empty = l_full + kLseRing;
+  uint64_t* k_full = l_empty + kLseRing;  // [2]
+  uint64_t* s_full = k_full + 2;          // [2][2] tile, buffer
+  uint64_t* s_empty = s_full + 4;         // [2][2]
+  uint64_t* drain = s_empty + 4;
+  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_sh = reinterpret_cast<int*>(tmem_base_sh + 1);
+  int* never_sh = abort_sh + 1;
+  static_assert((2 * STAGES + 2 * kLseRing + 11) * 8 + 12 <= 256, "barrier area");
+
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x % p.split;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    w += part;
+    for (int s = 0; s < kLseRing; ++s) {
+      mbar_init(&l_full[s], 1);
+      mbar_init(&l_empty[s], 8);
+    }
+    for (int t = 0; t < 2; ++t) mbar_init(&k_full[t], 1);
+    for (int t = 0; t < 4; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&s_empty[t], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_sh = 0;
+    *never_sh = 0;
+    fence_mbar_init();
   }
-  if (k < s.k1) {
-    if (!isfinite(w)) status_or(a.status, RMM_NONFINITE_BIT);
-    const int64_t at = h * a.T_k + k;
-    a.w_out[at] = a.w_in ? a.w_in[at] + w : w;
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
   }
+  if (warp == 8) {
+    tmem_alloc<1>(tmem_base_sh, 512);
+    tmem_relinquish<1>();
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_sh;
+  pdl_wait();
+  volatile int* abort_v = abort_sh;
+  const volatile int* never_v = never_sh;
+  const uint64_t limit = a.wait_limit_ns;
+
+  const uint32_t unit = blockIdx.x / p.split;
+  const Work w = find_work<true>(a, unit / uint32_t(a.h_kv), 2 * kRows, lane);
+  const int32_t h = int32_t(unit % uint32_t(a.h_kv));
+  float total = 0.f;
+  if (w.tile >= 0) {
+    const int32_t S_q = w.s.q1 - w.s.q0, S_k = w.s.k1 - w.s.k0;
+    const int32_t off = S_k - S_q;
+    const int32_t n_qt = (S_q + p.nq_tile - 1) / p.nq_tile;
+    // key tile t: its first query tile of this CTA (n_qt on: none), and of the CTA
+    int32_t i0[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int32_t k = w.tile * 2 * kRows + t * kRows;
+      int32_t first = n_qt;
+      if (k < S_k) first = a.causal ? min(max(k - off, 0) / p.nq_tile, n_qt) : 0;
+      i0[t] = first + int32_t((rank + p.split - uint32_t(first) % p.split) % p.split);  // next one of this rank
+    }
+    const int32_t begin = min(i0[0], i0[1]), step = int32_t(p.split);
+
+    if (warp == 9) {
+      if (lane == 0 && begin < n_qt) {
+        bool ok = true;
+        uint32_t issued = 0, issued_par = 0;
+        for (int t = 0; t < 2; ++t) {
+          if (i0[t] >= n_qt) continue;
+          mbar_arrive_expect_tx(&k_full[t], Cfg::TILE);
+#pragma unroll
+          for (int x = 0; x < Cfg::BOXES; ++x)
+            tma_load_3d(sK + t * Cfg::TILE + x * Cfg::BOX, &tmK, &k_full[t], x * 64, h,
+                        w.s.k0 + w.tile * 2 * kRows + t * kRows);
+        }
+        uint32_t stage = 0, phase = 0;
+        for (int32_t i = begin; i < n_qt; i += step) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, limit, abort_v)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[stage], uint32_t(Cfg::BOXES * p.row_bytes));
+#pragma unroll
+          for (int x = 0; x < Cfg::BOXES; ++x)
+            tma_load_3d(sQ + stage * Cfg::TILE + x * Cfg::BOX, &tmQ, &full[stage], x * 64, h * p.g,
+                        w.s.q0 + i * p.nq_tile);
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) raise_abort(abort_v, a.status);
+        // no load may still be writing shared memory when the CTA exits
+        for (int t = 0; t < 2; ++t)
+          if (i0[t] < n_qt) mbar_wait_bounded(&k_full[t], 0, limit, never_v);
+        for (int s = 0; s < STAGES; ++s)
+          if (issued & (1u << s)) mbar_wait_bounded(&full[s], (issued_par >> s) & 1u, limit, never_v);
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      const uint32_t id_s = umma_idesc_bf16_f32(kRows, kRows, false);
+      const int ksteps = int((a.d + 15) / 16);
+      bool ok = true;
+      uint32_t stage = 0, phase = 0, par[2] = {0u, 0u}, seen[2] = {0u, 0u};
+      for (int32_t i = begin; ok && i < n_qt; i += step) {
+        ok = warp_wait(&full[stage], phase, limit, abort_v);
+        for (int t = 0; ok && t < 2; ++t) {
+          if (i < i0[t]) continue;
+          if (!seen[t]) {
+            ok = warp_wait(&k_full[t], 0, limit, abort_v);
+            if (!ok) break;
+          }
+          const uint32_t buf = seen[t]++ & 1u;
+          // a buffer's first use needs no wait
+          if (seen[t] > 2) {
+            ok = warp_wait(&s_empty[t * 2 + buf], (par[t] >> buf) & 1u, limit, abort_v);
+            if (!ok) break;
+            par[t] ^= 1u << buf;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t q = smem_addr(sQ + stage * Cfg::TILE), k = smem_addr(sK + t * Cfg::TILE);
+            for (int kk = 0; kk < ksteps; ++kk) {
+              const uint32_t o = uint32_t(kk >> 2) * Cfg::BOX + uint32_t(kk & 3) * 32;
+              umma_bf16<1>(tmem + (t * 2 + buf) * 128, umma_desc_k_sw128(k + o), umma_desc_k_sw128(q + o), id_s,
+                           kk != 0);
+            }
+            umma_commit<1>(smem_addr(&s_full[t * 2 + buf]));
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) umma_commit<1>(smem_addr(&empty[stage]));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (lane == 0) {
+        if (!ok) raise_abort(abort_v, a.status);
+        umma_commit<1>(smem_addr(drain));
+        mbar_wait_bounded(drain, 0, limit, never_v);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      bool ok = true;
+      uint32_t r = 0, phase = 0;
+      for (int32_t i = begin; i < n_qt; i += step) {
+        const int32_t q0 = i * p.nq_tile;
+        const int32_t live = min(p.nq_tile, S_q - q0) * p.g;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t c = 32 * e + lane;
+          v[e] = c < live ? a.lse[int64_t(h * p.g + c % p.g) * a.T_q + w.s.q0 + q0 + c / p.g] : 0.f;
+        }
+        if (!warp_wait(&l_empty[r], phase ^ 1u, limit, abort_v)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lse_sh[r * kRows + 32 * e + lane] = -v[e] * kLog2e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&l_full[r]);
+        if (++r == kLseRing) {
+          r = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok && lane == 0) raise_abort(abort_v, a.status);
+    } else {
+      const int t = warp >> 2;
+      const int r = (warp & 3) * 32 + lane;
+      const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + t * 256;
+      const int32_t k = w.tile * 2 * kRows + t * kRows + r;
+      const float2 c2 = make_float2(a.scale * kLog2e, a.scale * kLog2e);
+      float comp = 0.f;
+      bool ok = true;
+      uint32_t ring = 0, l_phase = 0, n = 0;
+      for (int32_t i = begin; i < n_qt; i += step) {
+        if (!warp_wait(&l_full[ring], l_phase, limit, abort_v)) {
+          ok = false;
+          break;
+        }
+        if (i >= i0[t]) {
+          const uint32_t buf = n & 1u, s_phase = (n >> 1) & 1u;
+          ++n;
+          if (!warp_wait(&s_full[t * 2 + buf], s_phase, limit, abort_v)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // pairs [lo, hi) of the tile count: queries that see this key, and that exist
+          const int32_t lo = a.causal ? (k - off - i * p.nq_tile) * p.g : 0;
+          const int32_t hi = min(p.nq_tile, S_q - i * p.nq_tile) * p.g;
+          const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < kRows;
+          const float* nl = lse_sh + ring * kRows;
+          float2 part[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) part[v] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t s[2][32];
+            tmem_ld_32x32b_x32(tS + buf * 128 + 64 * x, s[0]);
+            tmem_ld_32x32b_x32(tS + buf * 128 + 64 * x + 32, s[1]);
+            tmem_ld_wait();
+            if (x == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_empty[t * 2 + buf]);
+            }
+            auto add_up = [&](auto mask) {
+#pragma unroll
+              for (int e = 0; e < 64; e += 4) {
+                const float4 l4 = *reinterpret_cast<const float4*>(nl + 64 * x + e);
+                const uint32_t* v = &s[e >> 5][e & 31];
+                float2 y[2] = {fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2,
+                                    make_float2(l4.x, l4.y)),
+                               fma2(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), c2,
+                                    make_float2(l4.z, l4.w))};
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  if constexpr (decltype(mask)::value) {  // whatever the product or its lse is
+                    const int col = 64 * x + e + 2 * z;
+                    if (col < lo || col >= hi) y[z].x = -INFINITY;
+                    if (col + 1 < lo || col + 1 >= hi) y[z].y = -INFINITY;
+                  }
+                  float2& sum = part[((e >> 1) + z) & 3];
+                  sum = add2(sum, make_float2(ex2(y[z].x), ex2(y[z].y)));
+                }
+              }
+            };
+            if (masked)
+              add_up(std::true_type());
+            else
+              add_up(std::false_type());
+          }
+          const float2 p2 = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+          // total + comp: the sum with the rounding of each addition carried along
+          const float y = __fsub_rn(__fadd_rn(p2.x, p2.y), comp);
+          const float z = __fadd_rn(total, y);
+          comp = __fsub_rn(__fsub_rn(z, total), y);
+          total = z;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&l_empty[ring]);
+        if (++ring == kLseRing) {
+          ring = 0;
+          l_phase ^= 1u;
+        }
+      }
+      if (!ok && lane == 0) raise_abort(abort_v, a.status);
+      sum_sh[t * kRows + r] = total;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc<1>(tmem, 512);
+  if (p.split > 1) cluster_sync_all();
+  if (w.tile >= 0) {
+    const int32_t per = 2 * kRows / int32_t(p.split);
+    const int32_t k = w.tile * 2 * kRows + int32_t(rank) * per + int32_t(threadIdx.x);
+    if (int32_t(threadIdx.x) < per && k < w.s.k1 - w.s.k0) {
+      const int32_t i = int32_t(rank) * per + int32_t(threadIdx.x);
+      float x = 0.f;
+      if (p.split == 1) {
+        x = sum_sh[i];
+      } else {
+        for (uint32_t r = 0; r < p.split; ++r) x += ld_cluster_f32(mapa_shared(smem_addr(sum_sh + i), r));
+      }
+      if (!isfinite(x)) status_or(a.status, RMM_NONFINITE_BIT);
+      const int64_t at = int64_t(h) * a.T_k + w.s.k0 + k;
+      a.w_out[at] = a.w_in ? a.w_in[at] + x : x;
+    }
+  }
+  if (p.split > 1) cluster_sync_all();  // no CTA leaves while another reads its sums
 }
 
 // ------------------------------------------------------------------ host side
@@ -580,12 +886,40 @@ cudaError_t launch_prompt(const TcArgs& p, cudaStream_t st, const char** why) {
                     dim3(0, 0, 0), tmQ, tmK, tmV, p);
 }
 
+template <int DP>
+cudaError_t launch_weights(TcArgs p, cudaStream_t st, const char** why) {
+  using Cfg = WeightCfg<DP>;
+  const AttnArgs& a = p.a;
+  CUtensorMap tmQ, tmK;
+  bool ok = encode_tokens(&tmK, a.k, a.T_k, a.h_kv, a.d, kRows, 1);
+  if (a.T_q > 0)
+    ok = ok && encode_tokens(&tmQ, a.q, a.T_q, a.h_q, a.d, uint32_t(p.nq_tile), uint32_t(p.g));
+  else
+    tmQ = tmK;  // no query is ever loaded
+  if (!ok) {
+    *why = "cuTensorMapEncodeTiled failed for Q or K";
+    return cudaErrorInvalidValue;
+  }
+  cudaError_t e = cudaFuncSetAttribute(attn_key_weights_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(Cfg::SMEM));
+  if (e != cudaSuccess) return e;
+  const int64_t span = 2 * kRows;
+  const int64_t units = (a.n_seq == 1 ? (a.T_k + span - 1) / span : a.T_k / span + a.n_seq) * a.h_kv;
+  // enough CTAs to even out the units' different lengths over 148 SMs, but at least 4 query tiles each
+  const int64_t q_tiles = (a.T_q / std::max<int64_t>(a.n_seq, 1)) / p.nq_tile;
+  p.split = 1;
+  while (p.split < 8 && units * p.split < 4 * 148 && q_tiles >= 8 * int64_t(p.split)) p.split *= 2;
+  return launch_pdl(attn_key_weights_kernel<DP>, dim3(unsigned(units * p.split)), dim3(kWtThreads), Cfg::SMEM, st,
+                    p.split > 1 ? dim3(p.split, 1, 1) : dim3(0, 0, 0), tmQ, tmK, p);
+}
+
 TcArgs tc_args(const AttnArgs& a) {
   TcArgs p;
   p.a = a;
   p.g = int32_t(a.h_q / a.h_kv);
   p.nq_tile = kRows / p.g;
   p.row_bytes = p.nq_tile * p.g * 128;
+  p.split = 1;
   return p;
 }
 
@@ -598,9 +932,11 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, cudaStream_t st, const char** 
   return a.d <= 64 ? launch_prompt<64>(p, st, why) : launch_prompt<128>(p, st, why);
 }
 
-cudaError_t launch_attn_key_weights(const AttnArgs& a, cudaStream_t st, const char**) {
-  return launch_pdl(attn_key_weights_kernel, dim3(unsigned((a.T_k + 127) / 128), unsigned(a.h_kv), unsigned(a.n_seq)),
-                    dim3(128), 0, st, dim3(0, 0, 0), a);
+cudaError_t launch_attn_key_weights(const AttnArgs& a, cudaStream_t st, const char** why) {
+  cudaError_t e = device_ok(why);
+  if (e != cudaSuccess) return e;
+  const TcArgs p = tc_args(a);
+  return a.d <= 64 ? launch_weights<64>(p, st, why) : launch_weights<128>(p, st, why);
 }
 
 }  // namespace rmm
