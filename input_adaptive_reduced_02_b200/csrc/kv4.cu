@@ -114,7 +114,7 @@ struct Kv4Dev {
   Kv4AttnArgs a;
   float* ml;      // [batch][h_q][max_splits][2] (maximum in log2 units, sum)
   float* po;      // [batch][h_q][max_splits][d] unnormalised
-  float* scores;  // [batch][h_q][cap] log2 units, or null
+  float* scores;  // [batch][h_kv][cap][h_q / h_kv] log2 units, or null
   int32_t split_len, max_splits;
 };
 
@@ -122,79 +122,427 @@ __device__ __forceinline__ int32_t seq_len(const Kv4AttnArgs& a, int64_t b) {
   return int32_t(min(max(int64_t(a.lens[b]), int64_t(0)), a.cap));
 }
 
-constexpr int kSimpleThreads = 128;
+// One CTA per (split of the tokens, key head, up to 8·NT of its query heads);
+// its warps take tiles of 16 tokens in turn, each with a running maximum, sum
+// and output of its own, joined at the end.
+//
+// Both products run on mma.sync (16 x 8 x 16; a step has a few query rows per
+// key head, an eighth of the smallest tcgen05 tile), transposed so that the
+// tokens or channels are the 16 rows and the heads the 8 columns, which lets
+// the codes go from their bytes to operand registers with shifts and masks:
+//   Sᵀ  A = codes of 16 tokens as f16 subnormals c·2^-24 (nibbles 0, 2 of a
+//       half-word) or 16c·2^-24 (1, 3), B = q as f16. The head's queries are
+//       scaled by a power of two to have their largest below 2^15, so bf16's 8
+//       bits fit f16 exactly over 28 binades below it. One accumulator per
+//       group of 32 channels, then S += step·acc + min·(sum of q), in f32.
+//   Oᵀ  A = codes of 16 channels as bf16 integers, B = p·step of the group in
+//       bf16 (any step's range), transposed by movmatrix; p·min adds up in f32.
+// A tile's bytes come by cp.async through a ring per warp, kKvStages - 1 tiles
+// ahead; rows past the length arrive as zeros.
+constexpr int kKvWarps = 8;
+constexpr int kKvStages = 4;
+constexpr float kKvRescale = 8.0f;  // log2 of the growth of p that is let through unscaled
 
-// One CTA per (split, query head, sequence): a thread a token for the scores,
-// then a thread a channel for the sums.
-__global__ void __launch_bounds__(kSimpleThreads) kv4_attn_split_kernel(const Kv4Dev p) {
-  __shared__ float q[kKv4MaxD];
-  __shared__ float pr[kSimpleThreads];
-  __shared__ float red[4];
+template <int NG>
+struct KvTile {
+  static constexpr int CODES = 16 * 16 * NG;  // bytes of 16 rows of codes
+  static constexpr int SCALES = 16 * 4 * NG;
+  static constexpr int BYTES = 2 * (CODES + SCALES);
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+               " {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+               " {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// (x & m) | o in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(o));
+  return r;
+}
+// nibble i of both half-words as bf16: 128 + c is 0x4300 + c there, and the difference is exact
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, int i) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), "r"(0x43004300u));
+  return r;
+}
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float step_of(uint32_t sm) { return __uint_as_float(sm << 16); }
+__device__ __forceinline__ float min_of(uint32_t sm) { return __uint_as_float(sm & 0xFFFF0000u); }
+
+// NW consecutive 32-bit words from shared memory, 4·NW-byte aligned (NW 1, 2, 4) or 4-byte (3)
+template <int NW>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[NW], const void* p) {
+  if constexpr (NW == 4) {
+    const uint4 v = *static_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (NW == 2) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = static_cast<const uint32_t*>(p)[i];
+  }
+}
+
+// half-word g of row a in the low half, of row b in the high half, g = 0 .. NG-1
+template <int NG>
+__device__ __forceinline__ void pair_halves(uint32_t (&w)[NG], const uint8_t* a, const uint8_t* b) {
+  if constexpr (NG % 2 == 0) {
+    uint32_t x[NG / 2], y[NG / 2];
+    lds_words<NG / 2>(x, a);
+    lds_words<NG / 2>(y, b);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) w[g] = __byte_perm(x[g / 2], y[g / 2], g % 2 ? 0x7632 : 0x5410);
+  } else {
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      w[g] = uint32_t(reinterpret_cast<const uint16_t*>(a)[g]) | uint32_t(reinterpret_cast<const uint16_t*>(b)[g]) << 16;
+  }
+}
+
+template <int NG, int NT>
+__global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split_kernel(const Kv4Dev p) {
+  using Tile = KvTile<NG>;
+  constexpr int D = 32 * NG, HEADS = 8 * NT;
+  extern __shared__ __align__(16) uint8_t kv_smem[];  // [warps][stages][tile], then the outputs
+  __shared__ float m_sh[kKvWarps][HEADS], l_sh[kKvWarps][HEADS];
+  static_assert(kKvStages * Tile::BYTES >= HEADS * D * 4, "a warp's ring holds its outputs at the end");
   pdl_trigger();
   pdl_wait();
   const Kv4AttnArgs& a = p.a;
-  const int split = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t hq = blockIdx.y, b = blockIdx.z;
-  const int64_t h = hq / (a.h_q / a.h_kv);
-  const int32_t d = int32_t(a.d), ng = d / 32;
-  if (split == 0 && hq == 0 && b == 0 && tid == 0) *static_cast<uint32_t*>(a.workspace) = 0u;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, j = lane & 3;
+  const int64_t item = blockIdx.y;
+  const int32_t gq = int32_t(a.h_q / a.h_kv);
+  const int64_t b = item / a.h_kv;
+  const int32_t head0 = int32_t(blockIdx.z) * HEADS;  // first of this CTA's heads within the group
+  const int64_t hq0 = (item % a.h_kv) * gq + head0;
+  const int32_t heads = min(HEADS, gq - head0);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) *static_cast<uint32_t*>(a.workspace) = 0u;
   const int32_t len = seq_len(a, b);
-  const int32_t t0 = split * p.split_len, t1 = min(len, t0 + p.split_len);
+  const int32_t t0 = int32_t(blockIdx.x) * p.split_len, t1 = min(len, t0 + p.split_len);
   if (t0 >= t1) return;
-  if (tid < d)
-    q[tid] = bf16_to_f32(static_cast<const uint16_t*>(a.q)[b * a.q_ss + hq * a.q_hs + tid]) *
-             (a.scale * 1.4426950408889634f);
-  __syncthreads();
-  const int64_t row0 = (b * a.h_kv + h) * a.cap;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int32_t base = t0; base < t1; base += kSimpleThreads) {
-    const int32_t t = base + tid;
-    float x = -INFINITY;
-    if (t < t1) {
-      x = 0.f;
-      const uint32_t* kc = reinterpret_cast<const uint32_t*>(a.c.kc) + (row0 + t) * (4 * ng);
-      const uint32_t* ks = reinterpret_cast<const uint32_t*>(a.c.ks) + (row0 + t) * ng;
-      for (int w = 0; w < ng; ++w) {
-        const float s = __uint_as_float(ks[w] << 16), mn = __uint_as_float(ks[w] & 0xFFFF0000u);
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t c = kc[j * ng + w];
-          for (int e = 0; e < 8; ++e) x += q[32 * w + 8 * j + e] * fmaf(s, float((c >> (4 * e)) & 15u), mn);
+  const int32_t tiles = (t1 - t0 + 15) / 16;
+  uint8_t* ring = kv_smem + warp * (kKvStages * Tile::BYTES);
+
+  const int64_t row0 = item * a.cap + t0;
+  const uint8_t* src[4] = {a.c.kc + row0 * (16 * NG), a.c.vc + row0 * (16 * NG),
+                           reinterpret_cast<const uint8_t*>(a.c.ks) + row0 * (4 * NG),
+                           reinterpret_cast<const uint8_t*>(a.c.vs) + row0 * (4 * NG)};
+  const int32_t rows = t1 - t0;
+  auto load = [&](int32_t tile, uint8_t* dst) {
+    const int32_t live = min(16, rows - 16 * tile);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int64_t off = int64_t(tile) * Tile::CODES;
+#pragma unroll
+      for (int c = lane; c < 16 * NG; c += 32)  // an even number of rows of 16·NG bytes: whole 16-byte pieces
+        cp_async16(dst + v * Tile::CODES + 16 * c, src[v] + off + (16 * c < live * 16 * NG ? 16 * c : 0),
+                   16 * c < live * 16 * NG ? 16 : 0);
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int64_t off = int64_t(tile) * Tile::SCALES;
+      uint8_t* d = dst + 2 * Tile::CODES + v * Tile::SCALES;
+      if constexpr (NG == 4) {  // a row is 16 bytes
+        if (lane < 16) cp_async16(d + 16 * lane, src[2 + v] + off + (lane < live ? 16 * lane : 0), lane < live ? 16 : 0);
+      } else {
+#pragma unroll
+        for (int c = lane; c < 16 * NG; c += 32)
+          cp_async4(d + 4 * c, src[2 + v] + off + (c < live * NG ? 4 * c : 0), c < live * NG ? 4 : 0);
+      }
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kKvStages - 1; ++s) {
+    const int32_t tile = warp + s * kKvWarps;
+    if (tile < tiles) load(tile, ring + s * Tile::BYTES);
+    cp_async_commit();
+  }
+
+  // Queries of head r (of each n tile), channels 32g + 8j .. + 7: the operand of Sᵀ.
+  // Then of heads 2j, 2j+1, what their scores are made of.
+  uint32_t qb[NT][NG][4];
+  float qs[NT][NG][2], fh[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool live = 8 * n + r < heads;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_ss + (hq0 + (live ? 8 * n + r : 0)) * a.q_hs;
+    uint32_t w[NG][4];
+    uint32_t big = 0;  // largest magnitude, as its bf16 bits
+    float sum[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const uint4 u = live ? *reinterpret_cast<const uint4*>(q + 32 * g + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+      w[g][0] = u.x, w[g][1] = u.y, w[g][2] = u.z, w[g][3] = u.w;
+      sum[g] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        big = max(big, max(w[g][e] & 0x7FFFu, (w[g][e] >> 16) & 0x7FFFu));
+        sum[g] += __uint_as_float(w[g][e] << 16) + __uint_as_float(w[g][e] & 0xFFFF0000u);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+#pragma unroll
+      for (int g = 0; g < NG; ++g) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], o);
+    }
+    // the power of two: largest query below 2^15 (a head of zeros, or of next to nothing, by 2^114)
+    const int32_t e = big ? max(int32_t(big >> 7) - 127 - 14, -114) : 0;
+    const float mul = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float f[8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f[2 * c] = __uint_as_float(w[g][c] << 16) * mul;
+        f[2 * c + 1] = __uint_as_float(w[g][c] & 0xFFFF0000u) * mul;
+      }
+      // nibbles (c, c + 4) share a register; odd ones arrive 16 times too large
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float k = c % 2 ? 0.0625f : 1.0f;
+        qb[n][g][c] = pack_f16x2(f[c] * k, f[c + 4] * k);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int from = 4 * (2 * j + x);  // a lane that holds head 2j + x
+      const int32_t eh = __shfl_sync(0xffffffffu, e, from);
+      const float down = __uint_as_float(uint32_t(127 - eh) << 23) * 0x1p-24f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) qs[n][g][x] = __shfl_sync(0xffffffffu, sum[g], from) * down;
+      fh[n][x] = a.scale * 1.4426950408889634f * 0x1p24f * __uint_as_float(uint32_t(127 + eh) << 23);
+    }
+  }
+
+  float o[NT][2 * NG][4], om[NT][NG][2], nm[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      nm[n][x] = INFINITY;  // minus the maximum: none yet
+      l[n][x] = 0.f;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      om[n][g][0] = om[n][g][1] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[n][2 * g][c] = o[n][2 * g + 1][c] = 0.f;
+    }
+  }
+
+  int stage = 0;
+  for (int32_t tile = warp; tile < tiles; tile += kKvWarps) {
+    {
+      const int32_t ahead = tile + (kKvStages - 1) * kKvWarps;
+      const int s = stage == 0 ? kKvStages - 1 : stage - 1;
+      if (ahead < tiles) load(ahead, ring + s * Tile::BYTES);
+      cp_async_commit();
+    }
+    cp_async_wait<kKvStages - 1>();
+    __syncwarp();
+    const uint8_t* buf = ring + stage * Tile::BYTES;
+    const uint8_t *kc = buf, *vc = buf + Tile::CODES, *ks = buf + 2 * Tile::CODES, *vs = ks + Tile::SCALES;
+    const int32_t tok = t0 + 16 * tile + r;  // tokens tok and tok + 8
+
+    // ---- scores
+    float t[NT][4];
+    {
+      uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
+      lds_words<NG>(w0, kc + r * (16 * NG) + j * (4 * NG));
+      lds_words<NG>(w1, kc + (r + 8) * (16 * NG) + j * (4 * NG));
+      lds_words<NG>(s0, ks + r * (4 * NG));
+      lds_words<NG>(s1, ks + (r + 8) * (4 * NG));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t h0 = w0[g] >> 8, h1 = w1[g] >> 8;
+        const uint32_t lo[4] = {w0[g] & 0x000F000Fu, w1[g] & 0x000F000Fu, w0[g] & 0x00F000F0u, w1[g] & 0x00F000F0u};
+        const uint32_t hi[4] = {h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x00F000F0u};
+        const float st0 = step_of(s0[g]), mn0 = min_of(s0[g]), st1 = step_of(s1[g]), mn1 = min_of(s1[g]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(c, lo, qb[n][g][0], qb[n][g][1]);
+          mma_f16(c, hi, qb[n][g][2], qb[n][g][3]);
+          t[n][0] = fmaf(c[0], st0, fmaf(qs[n][g][0], mn0, t[n][0]));
+          t[n][1] = fmaf(c[1], st0, fmaf(qs[n][g][1], mn0, t[n][1]));
+          t[n][2] = fmaf(c[2], st1, fmaf(qs[n][g][0], mn1, t[n][2]));
+          t[n][3] = fmaf(c[3], st1, fmaf(qs[n][g][1], mn1, t[n][3]));
         }
       }
-      if (p.scores) p.scores[(b * a.h_q + hq) * a.cap + t] = x;
     }
-    float mx = x;
+    const bool in0 = tok < t1, in1 = tok + 8 < t1;
+    if (p.scores) {
+      float* dst = p.scores + (item * a.cap + tok) * gq + head0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float m2 = fmaxf(m, mx);
-    const float corr = exp2f(m - m2);
-    pr[tid] = t < t1 ? exp2f(x - m2) : 0.f;
-    __syncthreads();
-    m = m2;
-    l *= corr;
-    acc *= corr;
-    const int32_t cnt = min(kSimpleThreads, t1 - base);
-    const int w = tid / 32, i = tid % 32 / 8, r = tid % 8;
-    for (int k = 0; k < cnt; ++k) {
-      l += pr[k];
-      if (tid < d) {
-        const int64_t row = row0 + base + k;
-        const uint32_t c = reinterpret_cast<const uint16_t*>(a.c.vc)[row * (8 * ng) + r * ng + w];
-        const uint32_t sm = reinterpret_cast<const uint32_t*>(a.c.vs)[row * ng + w];
-        acc += pr[k] * fmaf(__uint_as_float(sm << 16), float((c >> (4 * i)) & 15u), __uint_as_float(sm & 0xFFFF0000u));
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (8 * n + 2 * j + x < heads) {
+            if (in0) dst[8 * n + 2 * j + x] = t[n][x] * fh[n][x];
+            if (in1) dst[8 * gq + 8 * n + 2 * j + x] = t[n][2 + x] * fh[n][x];
+          }
+    }
+    // ---- softmax: p = 2^(t·fh - maximum), the maximum one the whole warp uses
+    float pr[NT][4];
+    bool grew = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float x = fmaf(t[n][c], fh[n][c & 1], nm[n][c & 1]);
+        pr[n][c] = (c < 2 ? in0 : in1) ? x : -INFINITY;
+        grew |= pr[n][c] > kKvRescale;
+      }
+    if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = fmaxf(in0 ? t[n][x] * fh[n][x] : -INFINITY, in1 ? t[n][2 + x] * fh[n][x] : -INFINITY);
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+          const float nm2 = fminf(nm[n][x], -mx);
+          const float f = ex2f(nm2 - nm[n][x]);  // 0 the first time
+          nm[n][x] = nm2;
+          l[n][x] *= f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            om[n][g][x] *= f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              o[n][2 * g + u][x] *= f;
+              o[n][2 * g + u][2 + x] *= f;
+            }
+          }
+          pr[n][x] = in0 ? fmaf(t[n][x], fh[n][x], nm2) : -INFINITY;
+          pr[n][2 + x] = in1 ? fmaf(t[n][2 + x], fh[n][x], nm2) : -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) pr[n][c] = ex2f(pr[n][c]);
+      l[n][0] += pr[n][0] + pr[n][2];
+      l[n][1] += pr[n][1] + pr[n][3];
+    }
+    // ---- values
+    uint32_t wl[NG], wh[NG], s0[NG], s1[NG];
+    pair_halves<NG>(wl, vc + (2 * j) * (16 * NG) + r * (2 * NG), vc + (2 * j + 1) * (16 * NG) + r * (2 * NG));
+    pair_halves<NG>(wh, vc + (2 * j + 8) * (16 * NG) + r * (2 * NG), vc + (2 * j + 9) * (16 * NG) + r * (2 * NG));
+    lds_words<NG>(s0, vs + r * (4 * NG));
+    lds_words<NG>(s1, vs + (r + 8) * (4 * NG));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float st0 = step_of(s0[g]), mn0 = min_of(s0[g]), st1 = step_of(s1[g]), mn1 = min_of(s1[g]);
+      uint32_t av[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        av[u][0] = codes_bf16(wl[g], 2 * u);
+        av[u][1] = codes_bf16(wl[g], 2 * u + 1);
+        av[u][2] = codes_bf16(wh[g], 2 * u);
+        av[u][3] = codes_bf16(wh[g], 2 * u + 1);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t b0 = movmatrix_trans(pack_bf16x2(pr[n][0] * st0, pr[n][1] * st0));
+        const uint32_t b1 = movmatrix_trans(pack_bf16x2(pr[n][2] * st1, pr[n][3] * st1));
+        om[n][g][0] = fmaf(pr[n][0], mn0, fmaf(pr[n][2], mn1, om[n][g][0]));
+        om[n][g][1] = fmaf(pr[n][1], mn0, fmaf(pr[n][3], mn1, om[n][g][1]));
+        mma_bf16(o[n][2 * g], av[0], b0, b1);
+        mma_bf16(o[n][2 * g + 1], av[1], b0, b1);
       }
     }
-    __syncthreads();
+    stage = stage + 1 == kKvStages ? 0 : stage + 1;
+    __syncwarp();  // the stage is free for the next load
   }
-  const int64_t part = (b * a.h_q + hq) * p.max_splits + split;
-  if (tid == 0) {
-    p.ml[2 * part] = m;
-    p.ml[2 * part + 1] = l;
+  cp_async_wait<0>();
+  __syncwarp();
+
+  // ---- join the warps. A warp without a tile has maximum -inf, sum and outputs 0.
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1) {
+        l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], s);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) om[n][g][x] += __shfl_xor_sync(0xffffffffu, om[n][g][x], s);
+      }
+      if (r == 0) {
+        m_sh[warp][8 * n + 2 * j + x] = -nm[n][x];
+        l_sh[warp][8 * n + 2 * j + x] = l[n][x];
+      }
+    }
+  float* mine = reinterpret_cast<float*>(ring);  // [HEADS][D]
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mine[(8 * n + 2 * j + (c & 1)) * D + 32 * g + 16 * u + 8 * (c >> 1) + r] = o[n][2 * g + u][c] + om[n][g][c & 1];
+  __syncthreads();
+  const int live_warps = min(kKvWarps, tiles);
+  for (int i = tid; i < heads * D; i += kKvWarps * 32) {
+    const int hd = i / D;
+    float m = -INFINITY;
+    for (int w = 0; w < live_warps; ++w) m = fmaxf(m, m_sh[w][hd]);
+    float sum = 0.f, out = 0.f;
+    for (int w = 0; w < live_warps; ++w) {
+      const float f = ex2f(m_sh[w][hd] - m);
+      sum += l_sh[w][hd] * f;
+      out += reinterpret_cast<const float*>(kv_smem + w * (kKvStages * Tile::BYTES))[i] * f;
+    }
+    const int64_t part = (b * a.h_q + hq0 + hd) * p.max_splits + blockIdx.x;
+    if (i % D == 0) {
+      p.ml[2 * part] = m;
+      p.ml[2 * part + 1] = sum;
+    }
+    p.po[part * D + i % D] = out;
   }
-  if (tid < d) p.po[part * d + tid] = acc;
 }
 
 // Joins the splits. Blocks [0, batch·h_q): O and the log-sum-exp of one head.
@@ -262,7 +610,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
   const int32_t t1 = min(len, t0 + kJoinTokens);
   for (int32_t t = t0 + tid; t < t1; t += kJoinThreads) {
     float s = 0.f;
-    for (int g = 0; g < gq; ++g) s += exp2f(p.scores[(head0 + g) * a.cap + t] - lse2[g]);
+    for (int g = 0; g < gq; ++g) s += exp2f(p.scores[(item * a.cap + t) * gq + g] - lse2[g]);
     const int64_t at = item * a.cap + t;
     a.w_out[at] = a.w_in ? a.w_in[at] + s : s;
   }
@@ -294,6 +642,19 @@ Kv4Ws kv4_ws(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, b
   return w;
 }
 
+namespace {
+template <int NG, int NT>
+cudaError_t launch_split(const Kv4Dev& p, const Kv4Ws& w, cudaStream_t st) {
+  constexpr int smem = kKvWarps * kKvStages * KvTile<NG>::BYTES;
+  cudaError_t e = cudaFuncSetAttribute(kv4_attn_split_kernel<NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t chunks = (p.a.h_q / p.a.h_kv + 8 * NT - 1) / (8 * NT);
+  return launch_pdl(kv4_attn_split_kernel<NG, NT>,
+                    dim3(unsigned(w.max_splits), unsigned(p.a.batch * p.a.h_kv), unsigned(chunks)), dim3(kKvWarps * 32),
+                    size_t(smem), st, dim3(0, 0, 0), p);
+}
+}  // namespace
+
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st) {
   const Kv4Ws w = kv4_ws(a.batch, a.h_q, a.h_kv, a.d, a.cap, a.w_out != nullptr);
   char* base = static_cast<char*>(a.workspace);
@@ -304,8 +665,14 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st) {
   p.scores = a.w_out ? reinterpret_cast<float*>(base + w.scores) : nullptr;
   p.split_len = int32_t(w.split_len);
   p.max_splits = int32_t(w.max_splits);
-  cudaError_t e = launch_pdl(kv4_attn_split_kernel, dim3(unsigned(w.max_splits), unsigned(a.h_q), unsigned(a.batch)),
-                             dim3(kSimpleThreads), 0, st, dim3(0, 0, 0), p);
+  cudaError_t e;
+  const bool one = a.h_q / a.h_kv <= 8;
+  switch (a.d / kKv4Group) {
+    case 1: e = one ? launch_split<1, 1>(p, w, st) : launch_split<1, 2>(p, w, st); break;
+    case 2: e = one ? launch_split<2, 1>(p, w, st) : launch_split<2, 2>(p, w, st); break;
+    case 3: e = one ? launch_split<3, 1>(p, w, st) : launch_split<3, 2>(p, w, st); break;
+    default: e = one ? launch_split<4, 1>(p, w, st) : launch_split<4, 2>(p, w, st); break;
+  }
   if (e != cudaSuccess) return e;
   const int64_t o_blocks = a.batch * a.h_q;
   const int64_t w_blocks = a.w_out ? a.batch * a.h_kv * ((a.cap + kJoinTokens - 1) / kJoinTokens) : 0;
