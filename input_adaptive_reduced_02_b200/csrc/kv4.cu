@@ -110,21 +110,27 @@ __global__ void __launch_bounds__(256) kv4_store_kernel(const Kv4StoreArgs a) {
 }
 
 // ---------------------------------------------------------------- attention
+// The work is the tiles of 16 tokens of every item (sequence, key head, chunk
+// of its query heads) with tokens, one item after the other; CTA c takes tiles
+// [c·per, (c+1)·per) of the line, whichever items they are of, so ragged
+// lengths leave no SM idle. A part of an item that one CTA works on is one
+// partial result, in slot c + item: both only grow along the line, so no two
+// share one.
 struct Kv4Dev {
   Kv4AttnArgs a;
-  float* ml;      // [batch][h_q][max_splits][2] (maximum in log2 units, sum)
-  float* po;      // [batch][h_q][max_splits][d] unnormalised
+  float* ml;      // [slots][heads of a chunk][2] (maximum in log2 units, sum)
+  float* po;      // [slots][heads of a chunk][d] unnormalised
   float* scores;  // [batch][h_kv][cap][h_q / h_kv] log2 units, or null
-  int32_t split_len, max_splits;
+  int64_t* line;  // [batch + 1] first tile of each sequence, then all tiles; [batch + 1] tiles per CTA
+  int32_t chunks, chunk_heads;  // per key head; query heads of a chunk
 };
 
 __device__ __forceinline__ int32_t seq_len(const Kv4AttnArgs& a, int64_t b) {
   return int32_t(min(max(int64_t(a.lens[b]), int64_t(0)), a.cap));
 }
 
-// One CTA per (split of the tokens, key head, up to 8·NT of its query heads);
-// its warps take tiles of 16 tokens in turn, each with a running maximum, sum
-// and output of its own, joined at the end.
+// A CTA's warps take the tiles of a part in turn, each with a running maximum,
+// sum and output of its own, joined at the part's end.
 //
 // Both products run on mma.sync (16 x 8 x 16; a step has a few query rows per
 // key head, an eighth of the smallest tcgen05 tile), transposed so that the
@@ -235,30 +241,88 @@ __device__ __forceinline__ void pair_halves(uint32_t (&w)[NG], const uint8_t* a,
   }
 }
 
+// Tiles of the line before sequence b0 + i for each thread i's first sequence, and all tiles.
+struct LinePos {
+  int64_t before, all;
+};
+__device__ __forceinline__ LinePos line_scan(int64_t mine, int64_t* warp_sums, int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  LinePos r = {incl - mine, 0};
+  for (int w = 0; w < kKvWarps; ++w) {
+    if (w < warp) r.before += warp_sums[w];
+    r.all += warp_sums[w];
+  }
+  return r;
+}
+
 template <int NG, int NT>
 __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split_kernel(const Kv4Dev p) {
   using Tile = KvTile<NG>;
   constexpr int D = 32 * NG, HEADS = 8 * NT;
   extern __shared__ __align__(16) uint8_t kv_smem[];  // [warps][stages][tile], then the outputs
   __shared__ float m_sh[kKvWarps][HEADS], l_sh[kKvWarps][HEADS];
+  __shared__ int64_t sums_sh[kKvWarps], b_sh, before_sh;
   static_assert(kKvStages * Tile::BYTES >= HEADS * D * 4, "a warp's ring holds its outputs at the end");
   pdl_trigger();
   pdl_wait();
   const Kv4AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, j = lane & 3;
-  const int64_t item = blockIdx.y;
   const int32_t gq = int32_t(a.h_q / a.h_kv);
-  const int64_t b = item / a.h_kv;
-  const int32_t head0 = int32_t(blockIdx.z) * HEADS;  // first of this CTA's heads within the group
-  const int64_t hq0 = (item % a.h_kv) * gq + head0;
-  const int32_t heads = min(HEADS, gq - head0);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) *static_cast<uint32_t*>(a.workspace) = 0u;
-  const int32_t len = seq_len(a, b);
-  const int32_t t0 = int32_t(blockIdx.x) * p.split_len, t1 = min(len, t0 + p.split_len);
-  if (t0 >= t1) return;
-  const int32_t tiles = (t1 - t0 + 15) / 16;
+  if (blockIdx.x == 0 && tid == 0) *static_cast<uint32_t*>(a.workspace) = 0u;
+
+  // ---- this CTA's stretch of the line: a thread adds up the tiles of consecutive sequences
+  const int64_t seq_items = a.h_kv * p.chunks;
+  int64_t pos, end;
+  {
+    const int64_t each = (a.batch + kKvWarps * 32 - 1) / (kKvWarps * 32);
+    const int64_t s0 = min(tid * each, a.batch), s1 = min(s0 + each, a.batch);
+    int64_t mine = 0;
+    for (int64_t i = s0; i < s1; ++i) mine += (seq_len(a, i) + 15) / 16 * seq_items;
+    const LinePos at = line_scan(mine, sums_sh, tid);
+    // at least as many tiles as an item has on average, up to one per warp: fewer partial results to join
+    const int64_t per = max(max((at.all + gridDim.x - 1) / int64_t(gridDim.x), int64_t(1)),
+                            min(int64_t(kKvWarps), (at.all + a.batch * seq_items - 1) / (a.batch * seq_items)));
+    pos = blockIdx.x * per;
+    end = min(pos + per, at.all);
+    int64_t before = at.before;
+    for (int64_t i = s0; i < s1; ++i) {
+      const int64_t n = (seq_len(a, i) + 15) / 16 * seq_items;
+      if (before <= pos && pos < before + n) {
+        b_sh = i;
+        before_sh = before;
+      }
+      if (blockIdx.x == 0) p.line[i] = before;
+      before += n;
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+      p.line[a.batch] = at.all;
+      p.line[a.batch + 1] = per;
+    }
+  }
+  if (pos >= end) return;
+  __syncthreads();
+  int64_t b = b_sh;
+  int32_t len = seq_len(a, b), item_tiles = (len + 15) / 16;
+  int64_t in_seq = (pos - before_sh) / item_tiles;  // item of the sequence: (key head, chunk)
+  int32_t first = int32_t(pos - before_sh - in_seq * item_tiles);
   uint8_t* ring = kv_smem + warp * (kKvStages * Tile::BYTES);
+
+  for (;;) {  // a part: tiles [first, first + tiles) of an item
+  const int32_t tiles = int32_t(min(int64_t(item_tiles - first), end - pos));
+  const int64_t item = b * a.h_kv + in_seq / p.chunks;
+  const int32_t head0 = int32_t(in_seq % p.chunks) * HEADS;  // first of the chunk's heads within the group
+  const int64_t hq0 = (item - b * a.h_kv) * gq + head0;
+  const int32_t heads = min(HEADS, gq - head0);
+  const int32_t t0 = 16 * first, t1 = min(len, t0 + 16 * tiles);
 
   const int64_t row0 = item * a.cap + t0;
   const uint8_t* src[4] = {a.c.kc + row0 * (16 * NG), a.c.vc + row0 * (16 * NG),
@@ -271,7 +335,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     for (int v = 0; v < 2; ++v) {
       const int64_t off = int64_t(tile) * Tile::CODES;
 #pragma unroll
-      for (int c = lane; c < 16 * NG; c += 32)  // an even number of rows of 16·NG bytes: whole 16-byte pieces
+      for (int c = lane; c < 16 * NG; c += 32)  // rows are whole 16-byte pieces
         cp_async16(dst + v * Tile::CODES + 16 * c, src[v] + off + (16 * c < live * 16 * NG ? 16 * c : 0),
                    16 * c < live * 16 * NG ? 16 : 0);
     }
@@ -536,28 +600,53 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       sum += l_sh[w][hd] * f;
       out += reinterpret_cast<const float*>(kv_smem + w * (kKvStages * Tile::BYTES))[i] * f;
     }
-    const int64_t part = (b * a.h_q + hq0 + hd) * p.max_splits + blockIdx.x;
+    const int64_t part = (blockIdx.x + b * seq_items + in_seq) * HEADS + hd;
     if (i % D == 0) {
       p.ml[2 * part] = m;
       p.ml[2 * part + 1] = sum;
     }
     p.po[part * D + i % D] = out;
   }
+  pos += tiles;
+  if (pos >= end) return;
+  first = 0;
+  if (++in_seq == seq_items) {
+    in_seq = 0;
+    do {
+      len = seq_len(a, ++b);  // pos < end: a sequence with tokens follows
+    } while (len == 0);
+    item_tiles = (len + 15) / 16;
+  }
+  __syncthreads();  // the outputs in shared memory are read
+  }
 }
 
-// Joins the splits. Blocks [0, batch·h_q): O and the log-sum-exp of one head.
-// The rest, w_out = w_in + the group's probabilities, 512 tokens each.
+// Joins the parts of each item. Blocks [0, batch·h_q): O and the log-sum-exp of
+// one head. The rest, w_out = w_in + the group's probabilities, 512 tokens each.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinTokens = 512;
 
-// max and sum over the splits of one head (log2 units): every thread gets both
-__device__ __forceinline__ float2 join_ml(const float* ml, int32_t splits, int lane) {
+// The slots of an item's parts: [first, last].
+struct Parts {
+  int64_t first, last;
+};
+__device__ __forceinline__ Parts item_parts(const Kv4Dev& p, int64_t b, int64_t in_seq, int32_t len) {
+  const int64_t per = p.line[p.a.batch + 1], item = b * p.a.h_kv * p.chunks + in_seq;
+  const int64_t tiles = (len + 15) / 16, start = p.line[b] + in_seq * tiles;
+  return Parts{item + start / per, item + (start + tiles - 1) / per};
+}
+
+// maximum and sum over the parts of one head (log2 units): every lane gets both
+__device__ __forceinline__ float2 join_ml(const Kv4Dev& p, Parts s, int32_t head, int lane) {
   float m = -INFINITY;
-  for (int s = lane; s < splits; s += 32) m = fmaxf(m, ml[2 * s]);
+  for (int64_t i = s.first + lane; i <= s.last; i += 32) m = fmaxf(m, p.ml[2 * (i * p.chunk_heads + head)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float l = 0.f;
-  for (int s = lane; s < splits; s += 32) l += ml[2 * s + 1] * exp2f(ml[2 * s] - m);
+  for (int64_t i = s.first + lane; i <= s.last; i += 32) {
+    const float2 x = reinterpret_cast<const float2*>(p.ml)[i * p.chunk_heads + head];
+    l += x.y * exp2f(x.x - m);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   return make_float2(m, l);
@@ -569,12 +658,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
   pdl_wait();
   const Kv4AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t gq = int32_t(a.h_q / a.h_kv);
   if (int64_t(blockIdx.x) < o_blocks) {
     const int64_t b = blockIdx.x / a.h_q, hq = blockIdx.x % a.h_q;
     const int32_t len = seq_len(a, b);
-    const int32_t splits = (len + p.split_len - 1) / p.split_len;
-    const int64_t part = (b * a.h_q + hq) * p.max_splits;
-    const float2 g = join_ml(p.ml + 2 * part, splits, lane);
+    const int32_t hg = int32_t(hq % gq), head = hg % p.chunk_heads;
+    const Parts parts = item_parts(p, b, hq / gq * p.chunks + hg / p.chunk_heads, len);
+    float2 g = make_float2(-INFINITY, 0.f);
+    if (len > 0) g = join_ml(p, parts, head, lane);
     if (tid == 0) {
       if (len > 0 && !(g.y > 0.f && g.y < INFINITY && isfinite(g.x)))
         status_or(static_cast<uint32_t*>(a.workspace), RMM_NONFINITE_BIT);
@@ -582,8 +673,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
     }
     if (tid < a.d) {
       float o = 0.f;
-      for (int s = 0; s < splits; ++s) o += p.po[(part + s) * a.d + tid] * exp2f(p.ml[2 * (part + s)] - g.x);
-      o = len > 0 ? o / g.y : 0.f;
+      if (len > 0) {
+#pragma unroll 4
+        for (int64_t i = parts.first; i <= parts.last; ++i) {
+          const int64_t at = i * p.chunk_heads + head;
+          o += p.po[at * a.d + tid] * exp2f(p.ml[2 * at] - g.x);
+        }
+        o /= g.y;
+      }
       const int64_t at = b * a.o_ss + hq * a.o_hs + tid;
       if (a.out == kBF16)
         static_cast<uint16_t*>(a.o)[at] = uint16_t(pack_bf16x2(o, 0.f));
@@ -593,17 +690,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
     return;
   }
   const int64_t i = blockIdx.x - o_blocks;
-  const int64_t chunks = (a.cap + kJoinTokens - 1) / kJoinTokens;
-  const int64_t item = i / chunks;
+  const int64_t pieces = (a.cap + kJoinTokens - 1) / kJoinTokens;
+  const int64_t item = i / pieces;
   const int64_t b = item / a.h_kv, h = item % a.h_kv;
   const int32_t len = seq_len(a, b);
-  const int32_t t0 = int32_t(i % chunks) * kJoinTokens;
+  const int32_t t0 = int32_t(i % pieces) * kJoinTokens;
   if (t0 >= len) return;
-  const int32_t gq = int32_t(a.h_q / a.h_kv);
-  const int32_t splits = (len + p.split_len - 1) / p.split_len;
-  const int64_t head0 = b * a.h_q + h * gq;
   for (int g = warp; g < gq; g += kJoinThreads / 32) {
-    const float2 ml = join_ml(p.ml + 2 * (head0 + g) * p.max_splits, splits, lane);
+    const Parts parts = item_parts(p, b, h * p.chunks + g / p.chunk_heads, len);
+    const float2 ml = join_ml(p, parts, g % p.chunk_heads, lane);
     if (lane == 0) lse2[g] = ml.x + log2f(ml.y);
   }
   __syncthreads();
@@ -625,17 +720,27 @@ cudaError_t launch_kv4_store(const Kv4StoreArgs& a, cudaStream_t st) {
   return launch_pdl(kv4_store_kernel<uint32_t>, grid, dim3(256), 0, st, dim3(0, 0, 0), a);
 }
 
+// CTAs of the decode step: as many as stay resident, two per SM (one with 16 heads' outputs in registers).
+static int64_t kv4_grid(int64_t items, int64_t cap, bool one) {
+  return std::min<int64_t>(one ? 2 * 148 : 148, items * ((cap + 15) / 16));
+}
+
 Kv4Ws kv4_ws(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, bool weights) {
   Kv4Ws w;
-  const int64_t want = batch * h_kv * cap / (148 * 4);
-  w.split_len = std::min<int64_t>(std::max<int64_t>((want + 63) / 64 * 64, 128), 1024);
-  w.max_splits = (cap + w.split_len - 1) / w.split_len;
+  const int64_t group = h_q / h_kv;
+  w.chunk_heads = group <= 8 ? 8 : 16;
+  w.chunks = (group + w.chunk_heads - 1) / w.chunk_heads;
+  const int64_t items = batch * h_kv * w.chunks;
+  w.grid = kv4_grid(items, cap, w.chunk_heads == 8);
+  const int64_t rows = (w.grid + items) * w.chunk_heads;
   auto al = [](int64_t x) { return (x + 1023) / 1024 * 1024; };
   int64_t off = 1024;
+  w.line = size_t(off);
+  off += al((batch + 2) * 8);
   w.ml = size_t(off);
-  off += al(batch * h_q * w.max_splits * 8);
+  off += al(rows * 8);
   w.o = size_t(off);
-  off += al(batch * h_q * w.max_splits * d * 4);
+  off += al(rows * d * 4);
   w.scores = size_t(off);
   if (weights) off += al(batch * h_q * cap * 4);
   w.bytes = size_t(off);
@@ -648,10 +753,8 @@ cudaError_t launch_split(const Kv4Dev& p, const Kv4Ws& w, cudaStream_t st) {
   constexpr int smem = kKvWarps * kKvStages * KvTile<NG>::BYTES;
   cudaError_t e = cudaFuncSetAttribute(kv4_attn_split_kernel<NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t chunks = (p.a.h_q / p.a.h_kv + 8 * NT - 1) / (8 * NT);
-  return launch_pdl(kv4_attn_split_kernel<NG, NT>,
-                    dim3(unsigned(w.max_splits), unsigned(p.a.batch * p.a.h_kv), unsigned(chunks)), dim3(kKvWarps * 32),
-                    size_t(smem), st, dim3(0, 0, 0), p);
+  return launch_pdl(kv4_attn_split_kernel<NG, NT>, dim3(unsigned(w.grid)), dim3(kKvWarps * 32), size_t(smem), st,
+                    dim3(0, 0, 0), p);
 }
 }  // namespace
 
@@ -663,10 +766,11 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st) {
   p.ml = reinterpret_cast<float*>(base + w.ml);
   p.po = reinterpret_cast<float*>(base + w.o);
   p.scores = a.w_out ? reinterpret_cast<float*>(base + w.scores) : nullptr;
-  p.split_len = int32_t(w.split_len);
-  p.max_splits = int32_t(w.max_splits);
+  p.line = reinterpret_cast<int64_t*>(base + w.line);
+  p.chunks = int32_t(w.chunks);
+  p.chunk_heads = int32_t(w.chunk_heads);
   cudaError_t e;
-  const bool one = a.h_q / a.h_kv <= 8;
+  const bool one = w.chunk_heads == 8;
   switch (a.d / kKv4Group) {
     case 1: e = one ? launch_split<1, 1>(p, w, st) : launch_split<1, 2>(p, w, st); break;
     case 2: e = one ? launch_split<2, 1>(p, w, st) : launch_split<2, 2>(p, w, st); break;
