@@ -140,9 +140,14 @@ __device__ __forceinline__ int32_t seq_len(const Kv4AttnArgs& a, int64_t b) {
 //       half-word) or 16c·2^-24 (1, 3), B = q as f16. The head's queries are
 //       scaled by a power of two to have their largest below 2^15, so bf16's 8
 //       bits fit f16 exactly over 28 binades below it. One accumulator per
-//       group of 32 channels, then S += step·acc + min·(sum of q), in f32.
-//   Oᵀ  A = codes of 16 channels as bf16 integers, B = p·step of the group in
-//       bf16 (any step's range), transposed by movmatrix; p·min adds up in f32.
+//       group of 32 channels, then S += step·acc in f32; min·(sum of q) of all
+//       groups is one more product, the sums cut into three bf16 parts.
+//   Oᵀ  A = codes of 16 channels as bf16 subnormals c·2^-133 or 16c·2^-133, B =
+//       2^64·p·step of the group in bf16, transposed by movmatrix; p·min adds
+//       up in f32. The 2^64 keeps the products normal f32 numbers for p·step
+//       from 2^-57 (smaller ones fade out) up to 2^62.
+// So a word of 8 codes costs one shift and four masks. What bounds the kernel
+// is the rate of such instructions, then HBM.
 // A tile's bytes come by cp.async through a ring per warp, kKvStages - 1 tiles
 // ahead; rows past the length arrive as zeros.
 constexpr int kKvWarps = 8;
@@ -169,32 +174,20 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
                " {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
                " {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-// (x & m) | o in one instruction
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(o));
-  return r;
-}
-// nibble i of both half-words as bf16: 128 + c is 0x4300 + c there, and the difference is exact
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, int i) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), "r"(0x43004300u));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ float ex2f(float x) {
@@ -263,6 +256,12 @@ __device__ __forceinline__ LinePos line_scan(int64_t mine, int64_t* warp_sums, i
   return r;
 }
 
+// ceil(x / y), without the long 64-bit division wherever 32 bits do
+__device__ __forceinline__ int64_t div_up(int64_t x, int64_t y) {
+  if (((x + y) | y) >> 32 == 0) return (uint32_t(x) + uint32_t(y) - 1u) / uint32_t(y);
+  return (x + y - 1) / y;
+}
+
 template <int NG, int NT>
 __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split_kernel(const Kv4Dev p) {
   using Tile = KvTile<NG>;
@@ -280,22 +279,22 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   if (blockIdx.x == 0 && tid == 0) *static_cast<uint32_t*>(a.workspace) = 0u;
 
   // ---- this CTA's stretch of the line: a thread adds up the tiles of consecutive sequences
-  const int64_t seq_items = a.h_kv * p.chunks;
+  const int32_t seq_items = int32_t(a.h_kv) * p.chunks;
   int64_t pos, end;
   {
     const int64_t each = (a.batch + kKvWarps * 32 - 1) / (kKvWarps * 32);
     const int64_t s0 = min(tid * each, a.batch), s1 = min(s0 + each, a.batch);
     int64_t mine = 0;
-    for (int64_t i = s0; i < s1; ++i) mine += (seq_len(a, i) + 15) / 16 * seq_items;
+    for (int64_t i = s0; i < s1; ++i) mine += int64_t((seq_len(a, i) + 15) / 16) * seq_items;
     const LinePos at = line_scan(mine, sums_sh, tid);
     // at least as many tiles as an item has on average, up to one per warp: fewer partial results to join
-    const int64_t per = max(max((at.all + gridDim.x - 1) / int64_t(gridDim.x), int64_t(1)),
-                            min(int64_t(kKvWarps), (at.all + a.batch * seq_items - 1) / (a.batch * seq_items)));
+    const int64_t per = max(max(div_up(at.all, gridDim.x), int64_t(1)),
+                            min(int64_t(kKvWarps), div_up(at.all, a.batch * seq_items)));
     pos = blockIdx.x * per;
     end = min(pos + per, at.all);
     int64_t before = at.before;
     for (int64_t i = s0; i < s1; ++i) {
-      const int64_t n = (seq_len(a, i) + 15) / 16 * seq_items;
+      const int64_t n = int64_t((seq_len(a, i) + 15) / 16) * seq_items;
       if (before <= pos && pos < before + n) {
         b_sh = i;
         before_sh = before;
@@ -312,8 +311,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   __syncthreads();
   int64_t b = b_sh;
   int32_t len = seq_len(a, b), item_tiles = (len + 15) / 16;
-  int64_t in_seq = (pos - before_sh) / item_tiles;  // item of the sequence: (key head, chunk)
-  int32_t first = int32_t(pos - before_sh - in_seq * item_tiles);
+  int32_t in_seq = int32_t(div_up(pos - before_sh + 1, item_tiles)) - 1;  // item of the sequence: (key head, chunk)
+  int32_t first = int32_t(pos - before_sh - int64_t(in_seq) * item_tiles);
   uint8_t* ring = kv_smem + warp * (kKvStages * Tile::BYTES);
 
   for (;;) {  // a part: tiles [first, first + tiles) of an item
@@ -323,33 +322,57 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   const int64_t hq0 = (item - b * a.h_kv) * gq + head0;
   const int32_t heads = min(HEADS, gq - head0);
   const int32_t t0 = 16 * first, t1 = min(len, t0 + 16 * tiles);
+  const int64_t slot = blockIdx.x + b * seq_items + in_seq;
 
+  // a lane's 16-byte pieces of a tile's codes (keys', then values') and pieces of its scales
   const int64_t row0 = item * a.cap + t0;
-  const uint8_t* src[4] = {a.c.kc + row0 * (16 * NG), a.c.vc + row0 * (16 * NG),
-                           reinterpret_cast<const uint8_t*>(a.c.ks) + row0 * (4 * NG),
-                           reinterpret_cast<const uint8_t*>(a.c.vs) + row0 * (4 * NG)};
+  constexpr int SP = NG == 4 ? 1 : NG;            // pieces of scales per lane: rows of 16 bytes are copied whole
+  constexpr int SB = NG == 4 ? 16 : 4;            // their bytes
+  const uint8_t *code_src[NG], *scale_src[SP];
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int c = lane + 32 * i;
+    code_src[i] = (c < 16 * NG ? a.c.kc + 16 * c : a.c.vc + 16 * (c - 16 * NG)) + row0 * (16 * NG);
+  }
+#pragma unroll
+  for (int i = 0; i < SP; ++i) {
+    const int c = (lane + 32 * i) * SB;
+    scale_src[i] = reinterpret_cast<const uint8_t*>(c < Tile::SCALES ? a.c.ks : a.c.vs) +
+                   (c < Tile::SCALES ? c : c - Tile::SCALES) + row0 * (4 * NG);
+  }
   const int32_t rows = t1 - t0;
   auto load = [&](int32_t tile, uint8_t* dst) {
-    const int32_t live = min(16, rows - 16 * tile);
+    const int64_t off = int64_t(tile) * Tile::CODES, soff = int64_t(tile) * Tile::SCALES;
+    const int32_t live = rows - 16 * tile;
+    uint8_t* to = dst + 16 * lane;
+    uint8_t* sto = dst + 2 * Tile::CODES + SB * lane;
+    if (live >= 16) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int64_t off = int64_t(tile) * Tile::CODES;
+      for (int i = 0; i < NG; ++i) cp_async16(to + 512 * i, code_src[i] + off, 16);
 #pragma unroll
-      for (int c = lane; c < 16 * NG; c += 32)  // rows are whole 16-byte pieces
-        cp_async16(dst + v * Tile::CODES + 16 * c, src[v] + off + (16 * c < live * 16 * NG ? 16 * c : 0),
-                   16 * c < live * 16 * NG ? 16 : 0);
+      for (int i = 0; i < SP; ++i) {
+        if constexpr (SB == 16)
+          cp_async16(sto, scale_src[i] + soff, 16);
+        else
+          cp_async4(sto + 32 * SB * i, scale_src[i] + soff, 4);
+      }
+      return;
     }
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int64_t off = int64_t(tile) * Tile::SCALES;
-      uint8_t* d = dst + 2 * Tile::CODES + v * Tile::SCALES;
-      if constexpr (NG == 4) {  // a row is 16 bytes
-        if (lane < 16) cp_async16(d + 16 * lane, src[2 + v] + off + (lane < live ? 16 * lane : 0), lane < live ? 16 : 0);
-      } else {
+    for (int i = 0; i < NG; ++i) {  // rows past the length: zeros, and an address within the cache
+      const int c = (lane + 32 * i) * 16, in_plane = c < Tile::CODES ? c : c - Tile::CODES;
+      const bool in = in_plane < live * 16 * NG;
+      cp_async16(to + 512 * i, in ? code_src[i] + off : code_src[i] + off - in_plane, in ? 16 : 0);
+    }
 #pragma unroll
-        for (int c = lane; c < 16 * NG; c += 32)
-          cp_async4(d + 4 * c, src[2 + v] + off + (c < live * NG ? 4 * c : 0), c < live * NG ? 4 : 0);
-      }
+    for (int i = 0; i < SP; ++i) {
+      const int c = (lane + 32 * i) * SB, in_plane = c < Tile::SCALES ? c : c - Tile::SCALES;
+      const bool in = in_plane < live * 4 * NG;
+      const uint8_t* src = scale_src[i] + soff - (in ? 0 : in_plane);
+      if constexpr (SB == 16)
+        cp_async16(sto, src, in ? 16 : 0);
+      else
+        cp_async4(sto + 32 * SB * i, src, in ? 4 : 0);
     }
   };
 #pragma unroll
@@ -362,13 +385,14 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   // Queries of head r (of each n tile), channels 32g + 8j .. + 7: the operand of Sᵀ.
   // Then of heads 2j, 2j+1, what their scores are made of.
   uint32_t qb[NT][NG][4];
-  float qs[NT][NG][2], fh[NT][2];
+  uint32_t qsum[NT][2];  // head r's sum of q over group j as three bf16 parts
+  float fh[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const bool live = 8 * n + r < heads;
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_ss + (hq0 + (live ? 8 * n + r : 0)) * a.q_hs;
     uint32_t w[NG][4];
-    uint32_t big = 0;  // largest magnitude, as its bf16 bits
+    uint32_t top = 0;  // largest magnitude, as its bf16 bits
     float sum[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -377,18 +401,18 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       sum[g] = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        big = max(big, max(w[g][e] & 0x7FFFu, (w[g][e] >> 16) & 0x7FFFu));
+        top = max(top, max(w[g][e] & 0x7FFFu, (w[g][e] >> 16) & 0x7FFFu));
         sum[g] += __uint_as_float(w[g][e] << 16) + __uint_as_float(w[g][e] & 0xFFFF0000u);
       }
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
       for (int g = 0; g < NG; ++g) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], o);
     }
     // the power of two: largest query below 2^15 (a head of zeros, or of next to nothing, by 2^114)
-    const int32_t e = big ? max(int32_t(big >> 7) - 127 - 14, -114) : 0;
+    const int32_t e = top ? max(int32_t(top >> 7) - 127 - 14, -114) : 0;
     const float mul = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -405,13 +429,18 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
         qb[n][g][c] = pack_f16x2(f[c] * k, f[c + 4] * k);
       }
     }
+    float qs = sum[0];
+#pragma unroll
+    for (int g = 1; g < NG; ++g)
+      if (j == g) qs = sum[g];
+    qs = j < NG ? qs * mul * 0x1p-24f : 0.f;
+    const uint32_t hi = pack_bf16x2(qs, 0.f) << 16;
+    const float rest = qs - __uint_as_float(hi);
+    qsum[n][0] = pack_bf16x2(qs, rest);
+    qsum[n][1] = pack_bf16x2(rest - __uint_as_float(qsum[n][0] & 0xFFFF0000u), 0.f);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int from = 4 * (2 * j + x);  // a lane that holds head 2j + x
-      const int32_t eh = __shfl_sync(0xffffffffu, e, from);
-      const float down = __uint_as_float(uint32_t(127 - eh) << 23) * 0x1p-24f;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) qs[n][g][x] = __shfl_sync(0xffffffffu, sum[g], from) * down;
+      const int32_t eh = __shfl_sync(0xffffffffu, e, 4 * (2 * j + x));  // a lane that holds head 2j + x
       fh[n][x] = a.scale * 1.4426950408889634f * 0x1p24f * __uint_as_float(uint32_t(127 + eh) << 23);
     }
   }
@@ -454,27 +483,34 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       lds_words<NG>(w1, kc + (r + 8) * (16 * NG) + j * (4 * NG));
       lds_words<NG>(s0, ks + r * (4 * NG));
       lds_words<NG>(s1, ks + (r + 8) * (4 * NG));
+      const int jg = NG == 4 ? j : min(j, NG - 1);
+      const uint32_t m0 = __byte_perm(*reinterpret_cast<const uint32_t*>(ks + r * (4 * NG) + 4 * jg), 0, 0x3232);
+      const uint32_t m1 = __byte_perm(*reinterpret_cast<const uint32_t*>(ks + (r + 8) * (4 * NG) + 4 * jg), 0, 0x3232);
+      const uint32_t mins[4] = {m0, m1, m0, m1};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+      for (int n = 0; n < NT; ++n) {
+        t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+        mma_bf16(t[n], mins, qsum[n][0], qsum[n][1]);
+      }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const uint32_t h0 = w0[g] >> 8, h1 = w1[g] >> 8;
         const uint32_t lo[4] = {w0[g] & 0x000F000Fu, w1[g] & 0x000F000Fu, w0[g] & 0x00F000F0u, w1[g] & 0x00F000F0u};
         const uint32_t hi[4] = {h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x00F000F0u};
-        const float st0 = step_of(s0[g]), mn0 = min_of(s0[g]), st1 = step_of(s1[g]), mn1 = min_of(s1[g]);
+        const float st0 = step_of(s0[g]), st1 = step_of(s1[g]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
           mma_f16(c, lo, qb[n][g][0], qb[n][g][1]);
           mma_f16(c, hi, qb[n][g][2], qb[n][g][3]);
-          t[n][0] = fmaf(c[0], st0, fmaf(qs[n][g][0], mn0, t[n][0]));
-          t[n][1] = fmaf(c[1], st0, fmaf(qs[n][g][1], mn0, t[n][1]));
-          t[n][2] = fmaf(c[2], st1, fmaf(qs[n][g][0], mn1, t[n][2]));
-          t[n][3] = fmaf(c[3], st1, fmaf(qs[n][g][1], mn1, t[n][3]));
+          t[n][0] = fmaf(c[0], st0, t[n][0]);
+          t[n][1] = fmaf(c[1], st0, t[n][1]);
+          t[n][2] = fmaf(c[2], st1, t[n][2]);
+          t[n][3] = fmaf(c[3], st1, t[n][3]);
         }
       }
     }
-    const bool in0 = tok < t1, in1 = tok + 8 < t1;
+    const bool in0 = tok < t1, in1 = tok + 8 < t1;  // false in a part's last tile only
     if (p.scores) {
       float* dst = p.scores + (item * a.cap + tok) * gq + head0;
 #pragma unroll
@@ -488,21 +524,29 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     }
     // ---- softmax: p = 2^(t·fh - maximum), the maximum one the whole warp uses
     float pr[NT][4];
-    bool grew = false;
+    float top = -INFINITY;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float x = fmaf(t[n][c], fh[n][c & 1], nm[n][c & 1]);
-        pr[n][c] = (c < 2 ? in0 : in1) ? x : -INFINITY;
-        grew |= pr[n][c] > kKvRescale;
+        pr[n][c] = fmaf(t[n][c], fh[n][c & 1], nm[n][c & 1]);
+        top = fmaxf(top, pr[n][c]);
       }
-    if (__any_sync(0xffffffffu, grew)) {
+    const bool tail = 16 * tile + 16 > rows;
+    if (__any_sync(0xffffffffu, tail || top > kKvRescale)) {
+      if (tail) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!(c < 2 ? in0 : in1)) t[n][c] = -INFINITY;
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float mx = fmaxf(in0 ? t[n][x] * fh[n][x] : -INFINITY, in1 ? t[n][2 + x] * fh[n][x] : -INFINITY);
+          // fh is positive; -inf stays out of the maximum, which some token of every tile reaches
+          float mx = fmaxf(t[n][x], t[n][2 + x]) * fh[n][x];
 #pragma unroll
           for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
           const float nm2 = fminf(nm[n][x], -mx);
@@ -518,8 +562,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
               o[n][2 * g + u][2 + x] *= f;
             }
           }
-          pr[n][x] = in0 ? fmaf(t[n][x], fh[n][x], nm2) : -INFINITY;
-          pr[n][2 + x] = in1 ? fmaf(t[n][2 + x], fh[n][x], nm2) : -INFINITY;
+          pr[n][x] = fmaf(t[n][x], fh[n][x], nm2);
+          pr[n][2 + x] = fmaf(t[n][2 + x], fh[n][x], nm2);
         }
     }
 #pragma unroll
@@ -530,6 +574,11 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       l[n][1] += pr[n][1] + pr[n][3];
     }
     // ---- values
+    float big[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) big[n][c] = pr[n][c] * 0x1p64f;
     uint32_t wl[NG], wh[NG], s0[NG], s1[NG];
     pair_halves<NG>(wl, vc + (2 * j) * (16 * NG) + r * (2 * NG), vc + (2 * j + 1) * (16 * NG) + r * (2 * NG));
     pair_halves<NG>(wh, vc + (2 * j + 8) * (16 * NG) + r * (2 * NG), vc + (2 * j + 9) * (16 * NG) + r * (2 * NG));
@@ -538,18 +587,13 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const float st0 = step_of(s0[g]), mn0 = min_of(s0[g]), st1 = step_of(s1[g]), mn1 = min_of(s1[g]);
-      uint32_t av[2][4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        av[u][0] = codes_bf16(wl[g], 2 * u);
-        av[u][1] = codes_bf16(wl[g], 2 * u + 1);
-        av[u][2] = codes_bf16(wh[g], 2 * u);
-        av[u][3] = codes_bf16(wh[g], 2 * u + 1);
-      }
+      const uint32_t hl = wl[g] >> 8, hh = wh[g] >> 8;
+      const uint32_t av[2][4] = {{wl[g] & 0x000F000Fu, wl[g] & 0x00F000F0u, wh[g] & 0x000F000Fu, wh[g] & 0x00F000F0u},
+                                 {hl & 0x000F000Fu, hl & 0x00F000F0u, hh & 0x000F000Fu, hh & 0x00F000F0u}};
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint32_t b0 = movmatrix_trans(pack_bf16x2(pr[n][0] * st0, pr[n][1] * st0));
-        const uint32_t b1 = movmatrix_trans(pack_bf16x2(pr[n][2] * st1, pr[n][3] * st1));
+        const uint32_t b0 = movmatrix_trans(pack_bf16x2(big[n][0] * st0, big[n][1] * st0));
+        const uint32_t b1 = movmatrix_trans(pack_bf16x2(big[n][2] * st1, big[n][3] * st1));
         om[n][g][0] = fmaf(pr[n][0], mn0, fmaf(pr[n][2], mn1, om[n][g][0]));
         om[n][g][1] = fmaf(pr[n][1], mn0, fmaf(pr[n][3], mn1, om[n][g][1]));
         mma_bf16(o[n][2 * g], av[0], b0, b1);
@@ -587,25 +631,33 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          mine[(8 * n + 2 * j + (c & 1)) * D + 32 * g + 16 * u + 8 * (c >> 1) + r] = o[n][2 * g + u][c] + om[n][g][c & 1];
+          mine[(8 * n + 2 * j + (c & 1)) * D + 32 * g + 16 * u + 8 * (c >> 1) + r] =
+              fmaf(o[n][2 * g + u][c], c < 2 ? 0x1p69f : 0x1p65f, om[n][g][c & 1]);
   __syncthreads();
-  const int live_warps = min(kKvWarps, tiles);
-  for (int i = tid; i < heads * D; i += kKvWarps * 32) {
-    const int hd = i / D;
-    float m = -INFINITY;
-    for (int w = 0; w < live_warps; ++w) m = fmaxf(m, m_sh[w][hd]);
-    float sum = 0.f, out = 0.f;
-    for (int w = 0; w < live_warps; ++w) {
-      const float f = ex2f(m_sh[w][hd] - m);
-      sum += l_sh[w][hd] * f;
-      out += reinterpret_cast<const float*>(kv_smem + w * (kKvStages * Tile::BYTES))[i] * f;
+  if (tid < heads) {  // m_sh becomes the warps' factors
+    float m = m_sh[0][tid];  // the first warp has a tile
+#pragma unroll
+    for (int w = 1; w < kKvWarps; ++w) m = fmaxf(m, m_sh[w][tid]);
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kKvWarps; ++w) {
+      const float f = ex2f(m_sh[w][tid] - m);
+      sum += l_sh[w][tid] * f;
+      m_sh[w][tid] = f;
     }
-    const int64_t part = (blockIdx.x + b * seq_items + in_seq) * HEADS + hd;
-    if (i % D == 0) {
-      p.ml[2 * part] = m;
-      p.ml[2 * part + 1] = sum;
+    *reinterpret_cast<float2*>(p.ml + 2 * (slot * HEADS + tid)) = make_float2(m, sum);
+  }
+  __syncthreads();
+  for (int i = 4 * tid; i < heads * D; i += 4 * kKvWarps * 32) {
+    float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kKvWarps; ++w) {
+      const float f = m_sh[w][i / D];
+      const float4 x = *reinterpret_cast<const float4*>(kv_smem + w * (kKvStages * Tile::BYTES) + 4 * i);
+      out.x = fmaf(x.x, f, out.x), out.y = fmaf(x.y, f, out.y);
+      out.z = fmaf(x.z, f, out.z), out.w = fmaf(x.w, f, out.w);
     }
-    p.po[part * D + i % D] = out;
+    *reinterpret_cast<float4*>(p.po + slot * (HEADS * D) + i) = out;
   }
   pos += tiles;
   if (pos >= end) return;
@@ -630,7 +682,7 @@ constexpr int kJoinTokens = 512;
 struct Parts {
   int64_t first, last;
 };
-__device__ __forceinline__ Parts item_parts(const Kv4Dev& p, int64_t b, int64_t in_seq, int32_t len) {
+__device__ __forceinline__ Parts item_parts(const Kv4Dev& p, int64_t b, int32_t in_seq, int32_t len) {
   const int64_t per = p.line[p.a.batch + 1], item = b * p.a.h_kv * p.chunks + in_seq;
   const int64_t tiles = (len + 15) / 16, start = p.line[b] + in_seq * tiles;
   return Parts{item + start / per, item + (start + tiles - 1) / per};
