@@ -319,9 +319,10 @@ rmm_status rmm_cache_evict(const float* w, const int32_t* lens, int64_t batch, i
   DeviceGuard dg;
   rmm_status r = bind_device(stream, dg);
   if (r) return r;
-  const cudaError_t ce = cudaMemsetAsync(workspace, 0, 4, stream);
-  if (ce != cudaSuccess) return cuda_fail(ce, "cudaMemsetAsync(status)");
-  if (batch == 0) return RMM_OK;
+  if (batch == 0) {
+    const cudaError_t ce = cudaMemsetAsync(workspace, 0, 4, stream);
+    return ce == cudaSuccess ? RMM_OK : cuda_fail(ce, "cudaMemsetAsync(status)");
+  }
   char* base = static_cast<char*>(workspace);
   a.w = w;
   a.lens = lens;
