@@ -30,82 +30,120 @@ __device__ __forceinline__ int64_t find_seq(const int32_t* cu, int64_t n, int64_
 }
 
 // ---------------------------------------------------------------- store
-// A thread quantises 8 channels, four neighbouring lanes a group.
+// A thread quantises 8 channels of a token's keys and of its values, four
+// neighbouring lanes a group, 4·NG a row; a block takes rows of one head.
+// Bound by HBM for whole prompts: 2·d values read, 2·(d/2 + d/8) bytes written.
+constexpr int kStoreThreads = 256;
+
+// rint(x / s) for x / s in about [-1, 17]: the product with the reciprocal is
+// within 2^-17 of the quotient, so only next to a half does it take the division.
+__device__ __forceinline__ float rounded_quotient(float x, float s, float inv) {
+  const float q = x * inv, r = rintf(q);
+  return fabsf(fabsf(q - r) - 0.5f) > 0x1p-15f ? r : rintf(__fdiv_rn(x, s));
+}
+
 template <typename T>
-__global__ void __launch_bounds__(256) kv4_store_kernel(const Kv4StoreArgs a) {
+__device__ __forceinline__ void load8(float (&f)[8], const T* p, bool vec) {
+  if (vec) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 u = reinterpret_cast<const float4*>(p)[h];
+        f[4 * h] = u.x, f[4 * h + 1] = u.y, f[4 * h + 2] = u.z, f[4 * h + 3] = u.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = elem_to_f32(p[e]);
+  }
+}
+
+template <typename T, int NG>
+__global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4StoreArgs a, bool vec) {
+  constexpr int LANES = 4 * NG, ROWS = kStoreThreads / LANES;
   pdl_trigger();
   pdl_wait();
-  const int32_t ng = int32_t(a.d / kKv4Group);
-  const int32_t per_row = 4 * ng;
-  const int64_t total = a.T * a.h_kv * 2 * per_row;
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t ic = i < total ? i : total - 1;  // surplus threads repeat the last unit and store nothing
-  const int32_t u = int32_t(ic % per_row);
-  int64_t r = ic / per_row;
-  const int kv = int(r & 1);
-  r >>= 1;
-  const int64_t h = r % a.h_kv, t = r / a.h_kv;
-  int64_t b = t, in_seq = 0;
-  bool live = i < total;
+  const int row = threadIdx.x / LANES, u = threadIdx.x % LANES;
+  const int64_t h = blockIdx.y;
+  const int64_t t = int64_t(blockIdx.x) * ROWS + row;
+  bool live = row < ROWS && t < a.T;
+  const int64_t tc = min(t, a.T - 1);  // surplus threads repeat the last token and store nothing
+  float f[2][8];
+  load8(f[0], static_cast<const T*>(a.k.ptr) + tc * a.k.ts + h * a.k.hs + 8 * u, vec);
+  load8(f[1], static_cast<const T*>(a.v.ptr) + tc * a.v.ts + h * a.v.hs + 8 * u, vec);
+  int64_t b = tc, in_seq = 0;
   if (a.cu) {
-    b = find_seq(a.cu, a.n_seq, t);
-    in_seq = t - a.cu[b];
-    live = live && in_seq >= 0 && t < a.cu[b + 1];
+    b = find_seq(a.cu, a.n_seq, tc);
+    in_seq = tc - a.cu[b];
+    live = live && in_seq >= 0 && tc < a.cu[b + 1];
   }
   const int64_t slot = int64_t(a.start[b]) + in_seq;
   const bool in_cache = slot >= 0 && slot < a.cap;
   const int w = u >> 2, j = u & 3;  // group, quarter of the group
-  const TokView& x = kv ? a.v : a.k;
-  const T* src = static_cast<const T*>(x.ptr) + t * x.ts + h * x.hs + 8 * u;
-  float f[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = elem_to_f32(src[e]);
-  float lo = f[0], hi = f[0];
+  const int64_t at = (b * a.h_kv + h) * a.cap + slot;
   bool bad = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    lo = fminf(lo, f[e]);
-    hi = fmaxf(hi, f[e]);
-    bad |= !isfinite(f[e]);
-  }
+  for (int kv = 0; kv < 2; ++kv) {
+    const float* x = f[kv];
+    float lo = x[0], hi = x[0];
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  // (step, minimum) as stored; IEEE divisions, so that the codes depend on nothing but the values
-  const uint32_t sm = pack_bf16x2(__fdiv_rn(hi - lo, 15.0f), lo);
-  const float step = __uint_as_float(sm << 16), mn = __uint_as_float(sm & 0xFFFF0000u);
-  uint32_t codes = 0;  // nibble e: channel 8u + e
+    for (int e = 0; e < 8; ++e) {
+      lo = fminf(lo, x[e]);
+      hi = fmaxf(hi, x[e]);
+      bad |= !isfinite(x[e]);
+    }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float q = step > 0.f ? rintf(__fdiv_rn(f[e] - mn, step)) : 0.f;
-    codes |= uint32_t(fminf(fmaxf(q, 0.f), 15.f)) << (4 * e);
-  }
-  // the values' half-words need one nibble from each of the group's four lanes
-  uint32_t half[2] = {0u, 0u};  // half-words r = 2j, 2j + 1 of group w
+    for (int o = 1; o < 4; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    // (step, minimum) as stored; the IEEE quotient, so that it depends on nothing but the values
+    const uint32_t sm = pack_bf16x2(__fdiv_rn(hi - lo, 15.0f), lo);
+    const float step = __uint_as_float(sm << 16), mn = __uint_as_float(sm & 0xFFFF0000u);
+    const float inv = 1.0f / step;
+    // a step whose reciprocal is no normal number takes the division throughout
+    const bool near = step > 0x1p-120f && step < 0x1p120f;
+    uint32_t codes = 0;  // nibble e: channel 8u + e
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const uint32_t c = __shfl_sync(0xffffffffu, codes, (threadIdx.x & 28) | s);
-    half[0] |= ((c >> (8 * j)) & 15u) << (4 * s);
-    half[1] |= ((c >> (8 * j + 4)) & 15u) << (4 * s);
+    for (int e = 0; e < 8; ++e) {
+      float q = 0.f;
+      if (step > 0.f) q = near ? rounded_quotient(x[e] - mn, step, inv) : rintf(__fdiv_rn(x[e] - mn, step));
+      codes |= uint32_t(fminf(fmaxf(q, 0.f), 15.f)) << (4 * e);
+    }
+    // the values' half-words need one nibble from each of the group's four lanes
+    uint32_t half[2] = {0u, 0u};  // half-words r = 2j, 2j + 1 of group w
+    if (kv == 1) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t c = __shfl_sync(0xffffffffu, codes, (threadIdx.x & 28) | s);
+        half[0] |= ((c >> (8 * j)) & 15u) << (4 * s);
+        half[1] |= ((c >> (8 * j + 4)) & 15u) << (4 * s);
+      }
+    }
+    if (!live || !in_cache) continue;
+    if (j == 0) reinterpret_cast<uint32_t*>(kv ? a.c.vs : a.c.ks)[at * NG + w] = sm;
+    if (kv == 0) {
+      reinterpret_cast<uint32_t*>(a.c.kc)[at * LANES + j * NG + w] = codes;
+    } else {
+      uint16_t* v = reinterpret_cast<uint16_t*>(a.c.vc) + at * (2 * LANES);
+      v[(2 * j) * NG + w] = uint16_t(half[0]);
+      v[(2 * j + 1) * NG + w] = uint16_t(half[1]);
+    }
   }
   if (!live) return;
   if (bad) status_or(a.status, RMM_NONFINITE_BIT);
   if (!in_cache) {
     status_or(a.status, RMM_RANGE_BIT);
-    return;
-  }
-  const int64_t row = (b * a.h_kv + h) * a.cap + slot;
-  uint32_t* scales = reinterpret_cast<uint32_t*>(kv ? a.c.vs : a.c.ks);
-  if (j == 0) scales[row * ng + w] = sm;
-  if (!kv) {
-    reinterpret_cast<uint32_t*>(a.c.kc)[row * per_row + j * ng + w] = codes;
-    if (u == 0 && a.w) a.w[row] = a.w_new ? a.w_new[h * a.T + t] : 0.f;
-  } else {
-    uint16_t* v = reinterpret_cast<uint16_t*>(a.c.vc) + row * (2 * per_row);
-    v[(2 * j) * ng + w] = uint16_t(half[0]);
-    v[(2 * j + 1) * ng + w] = uint16_t(half[1]);
+  } else if (u == 0 && a.w) {
+    a.w[at] = a.w_new ? a.w_new[h * a.T + t] : 0.f;
   }
 }
 
@@ -765,11 +803,25 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
 
 }  // namespace
 
+namespace {
+template <typename T>
+cudaError_t launch_store(const Kv4StoreArgs& a, cudaStream_t st) {
+  constexpr int64_t per = 16 / sizeof(T);  // elements of a 16-byte load
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.k.ptr) | reinterpret_cast<uintptr_t>(a.v.ptr)) & 15u) == 0 &&
+                   (a.T == 1 || (a.k.ts | a.v.ts) % per == 0) && (a.h_kv == 1 || (a.k.hs | a.v.hs) % per == 0);
+  const int64_t rows = kStoreThreads / (a.d / 8);
+  const dim3 grid(unsigned((a.T + rows - 1) / rows), unsigned(a.h_kv)), block(kStoreThreads), none(0, 0, 0);
+  switch (a.d / kKv4Group) {
+    case 1: return launch_pdl(kv4_store_kernel<T, 1>, grid, block, 0, st, none, a, vec);
+    case 2: return launch_pdl(kv4_store_kernel<T, 2>, grid, block, 0, st, none, a, vec);
+    case 3: return launch_pdl(kv4_store_kernel<T, 3>, grid, block, 0, st, none, a, vec);
+    default: return launch_pdl(kv4_store_kernel<T, 4>, grid, block, 0, st, none, a, vec);
+  }
+}
+}  // namespace
+
 cudaError_t launch_kv4_store(const Kv4StoreArgs& a, cudaStream_t st) {
-  const int64_t total = a.T * a.h_kv * 2 * (a.d / 8);
-  const dim3 grid(unsigned((total + 255) / 256));
-  if (a.in == kBF16) return launch_pdl(kv4_store_kernel<uint16_t>, grid, dim3(256), 0, st, dim3(0, 0, 0), a);
-  return launch_pdl(kv4_store_kernel<uint32_t>, grid, dim3(256), 0, st, dim3(0, 0, 0), a);
+  return a.in == kBF16 ? launch_store<uint16_t>(a, st) : launch_store<uint32_t>(a, st);
 }
 
 // CTAs of the decode step: as many as stay resident, two per SM (one with 16 heads' outputs in registers).
