@@ -13,6 +13,7 @@ pages' activation-only column norm is mode "a_only".
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -144,12 +145,13 @@ def _out_code(dt: torch.dtype) -> int:
     raise TypeError(f"unsupported output dtype {dt}")
 
 
-def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+def _stream(t: torch.Tensor) -> int:
+    """The handle of the current stream of t's device (a small call's time is the host's, so no Stream object is made)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _mat(t: torch.Tensor, name: str):
@@ -424,7 +426,7 @@ def matmul_reduced(A: torch.Tensor, B: torch.Tensor, rho: float, mode: str = "pr
     _, _, _, ldc, sC = _mat(out, "C")
     _check(lib().rmm_matmul_reduced_batched(_ptr(A), lda, sA, _ptr(B), ldb, sB, int(b_kmajor), ba, M, K, N,
                                             float(rho), _dtype(A), SCORE_MODES[mode], _ptr(out), ldc, sC,
-                                            _out_code(out.dtype), _ptr(idx_out), ctypes.c_void_p(ws.ptr),
+                                            _out_code(out.dtype), _ptr(idx_out), ws.ptr,
                                             ws.nbytes, _stream(A)))
     return out, ws
 
@@ -445,7 +447,7 @@ def matmul_reduced_b_norms(A: torch.Tensor, B: torch.Tensor, b_norm: torch.Tenso
     _, _, _, ldc, sC = _mat(out, "C")
     _check(lib().rmm_matmul_reduced_b_norms(_ptr(A), lda, sA, _ptr(B), ldb, sB, int(b_kmajor), _ptr(b_norm),
                                             stride, ba, M, K, N, float(rho), _dtype(A), _ptr(out), ldc, sC,
-                                            _out_code(out.dtype), _ptr(idx_out), ctypes.c_void_p(ws.ptr),
+                                            _out_code(out.dtype), _ptr(idx_out), ws.ptr,
                                             ws.nbytes, _stream(A)))
     return out, ws
 
@@ -532,7 +534,7 @@ def matmul_reduced_w8(A: torch.Tensor, Wq: torch.Tensor, scale: torch.Tensor, rh
     _, _, _, ldc, sC = _mat(out, "C")
     _check(lib().rmm_matmul_reduced_w8(_ptr(A), lda, sA, _ptr(Wq), ldw, sW, _ptr(scale), ss, _ptr(b_norm), bn_stride,
                                        ba, M, K, N, float(rho), _dtype(A), SCORE_MODES[mode], _ptr(out), ldc, sC,
-                                       _out_code(out.dtype), _ptr(idx_out), ctypes.c_void_p(ws.ptr), ws.nbytes,
+                                       _out_code(out.dtype), _ptr(idx_out), ws.ptr, ws.nbytes,
                                        _stream(A)))
     return out, ws
 
@@ -548,7 +550,7 @@ def qk_reduced(Q: torch.Tensor, Kmat: torch.Tensor, rho: float, mode: str = "pro
     if out is None:
         out = torch.empty(bh, S_q, S_k, dtype=out_dtype, device=Q.device)
     _check(lib().rmm_qk_reduced(_ptr(Q), _ptr(Kmat), bh, S_q, S_k, d, float(rho), _dtype(Q), SCORE_MODES[mode],
-                                _ptr(out), _out_code(out.dtype), _ptr(idx_out), ctypes.c_void_p(ws.ptr), ws.nbytes,
+                                _ptr(out), _out_code(out.dtype), _ptr(idx_out), ws.ptr, ws.nbytes,
                                 _stream(Q)))
     return out, ws
 
@@ -564,7 +566,7 @@ def pv_reduced(P: torch.Tensor, V: torch.Tensor, rho: float, mode: str = "produc
     if out is None:
         out = torch.empty(bh, S_q, d, dtype=out_dtype, device=P.device)
     _check(lib().rmm_pv_reduced(_ptr(P), _ptr(V), bh, S_q, S_k, d, float(rho), _dtype(P), SCORE_MODES[mode],
-                                _ptr(out), _out_code(out.dtype), _ptr(idx_out), ctypes.c_void_p(ws.ptr), ws.nbytes,
+                                _ptr(out), _out_code(out.dtype), _ptr(idx_out), ws.ptr, ws.nbytes,
                                 _stream(P)))
     return out, ws
 
@@ -625,7 +627,7 @@ def pv_softmax_reduced(L: torch.Tensor, V: torch.Tensor, rho: float, scale: floa
         out = torch.empty(bh, S_q, d, dtype=out_dtype, device=L.device)
     _check(lib().rmm_pv_softmax_reduced(_ptr(L), _dtype(L), float(scale), int(causal), _ptr(V), bh, S_q, S_k, d,
                                         float(rho), SCORE_MODES[mode], _ptr(P), _ptr(out), _out_code(out.dtype),
-                                        _ptr(idx_out), ctypes.c_void_p(ws.ptr), ws.nbytes, _stream(L)))
+                                        _ptr(idx_out), ws.ptr, ws.nbytes, _stream(L)))
     return out, P, ws
 
 
@@ -637,9 +639,10 @@ def _tokens(t: torch.Tensor, name: str):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens][heads][d]")
     n, h, d = t.shape
-    if d > 1 and t.stride(2) != 1:
+    ts, hs, es = t.stride()
+    if d > 1 and es != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
-    return n, h, d, t.stride(0) if n > 1 else h * d, t.stride(1) if h > 1 else d
+    return n, h, d, ts if n > 1 else h * d, hs if h > 1 else d
 
 
 def _i32_vec(t: torch.Tensor, name: str, n: int, device):
@@ -650,7 +653,7 @@ def _i32_vec(t: torch.Tensor, name: str, n: int, device):
 
 def _f32_shape(t: torch.Tensor | None, name: str, shape, device):
     if t is not None and (t.dtype != torch.float32 or t.device != device or not t.is_contiguous()
-                          or tuple(t.shape) != tuple(shape)):
+                          or t.shape != shape):
         raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor on {device}")
     return t
 
@@ -736,12 +739,13 @@ class KV4Cache:
         self.batch, self.heads, self.cap, half = kc.shape
         self.d = 2 * half
         scales = (self.batch, self.heads, self.cap, self.d // KV4_GROUP, 2)
+        device = kc.device
         for name, t, dt, shape in (("kc", kc, torch.uint8, kc.shape), ("vc", vc, torch.uint8, kc.shape),
                                    ("ks", ks, torch.bfloat16, scales), ("vs", vs, torch.bfloat16, scales)):
-            if t.dtype != dt or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != kc.device:
-                raise ValueError(f"{name} must be a contiguous {dt} {list(shape)} tensor on {kc.device}")
+            if t.dtype != dt or t.shape != shape or not t.is_contiguous() or t.device != device:
+                raise ValueError(f"{name} must be a contiguous {dt} {list(shape)} tensor on {device}")
         self.kc, self.ks, self.vc, self.vs = kc, ks, vc, vs
-        self.w = _f32_shape(w, "w", (self.batch, self.heads, self.cap), kc.device)
+        self.w = _f32_shape(w, "w", (self.batch, self.heads, self.cap), device)
 
     @classmethod
     def empty(cls, batch: int, heads: int, cap: int, d: int, device="cuda", weights: bool = True) -> "KV4Cache":
@@ -782,6 +786,7 @@ def kv4_store(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, start: torch.Te
     return cache
 
 
+@functools.lru_cache(maxsize=1024)
 def kv4_attn_workspace_size(batch: int, h_q: int, h_kv: int, d: int, cap: int, weights: bool = False) -> int:
     return int(lib().rmm_kv4_attn_workspace_size(batch, h_q, h_kv, d, cap, int(weights)))
 
@@ -812,15 +817,12 @@ def kv4_attn(Q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, scale: float 
     _check(lib().rmm_kv4_attn(_ptr(Q), q_ss, q_hs, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs),
                               _ptr(lens), n, h_q, cache.heads, d, cache.cap,
                               float(d ** -0.5 if scale is None else scale), _dtype(Q), _ptr(out), o_ss, o_hs,
-                              _out_code(out.dtype), _ptr(lse), _ptr(w_in), _ptr(w_out), ctypes.c_void_p(ws.ptr),
+                              _out_code(out.dtype), _ptr(lse), _ptr(w_in), _ptr(w_out), ws.ptr,
                               ws.nbytes, _stream(Q)))
     return out, lse, ws
 
 
-class _Plane(ctypes.Structure):
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
-
-
+@functools.lru_cache(maxsize=1024)
 def cache_evict_workspace_size(batch: int, heads: int, budget: int) -> int:
     return int(lib().rmm_cache_evict_workspace_size(batch, heads, budget))
 
@@ -840,22 +842,27 @@ def cache_evict(w: torch.Tensor, lens: torch.Tensor, planes, budget: int, sink: 
         raise ValueError("w must be a contiguous float32 [batch][heads][cap] CUDA tensor")
     batch, heads, cap = w.shape
     _i32_vec(lens, "lens", batch, w.device)
-    pairs = [p if isinstance(p, tuple) else (p, p) for p in planes]
-    caps = {d.shape[2] for _, d in pairs if d.dim() >= 3}
-    if len(caps) > 1:
-        raise ValueError("the planes' destinations disagree on their capacity")
-    cap_out = caps.pop() if caps else max(cap, int(budget))
-    arr = (_Plane * max(1, len(pairs)))()
-    for i, (src, dst) in enumerate(pairs):
-        if (src.dim() < 3 or tuple(src.shape[:3]) != (batch, heads, cap) or src.dtype != dst.dtype
-                or tuple(dst.shape) != (batch, heads, cap_out, *src.shape[3:])
-                or not src.is_contiguous() or not dst.is_contiguous()
-                or src.device != w.device or dst.device != w.device):
-            raise ValueError(f"plane {i}: src and dst must be contiguous [batch][heads][cap][...] tensors like w")
+    head, device = (batch, heads, cap), w.device
+    cap_out, vals = None, []
+    for i, pair in enumerate(planes):
+        src, dst = pair if isinstance(pair, tuple) else (pair, pair)
+        shape, out_shape = src.shape, dst.shape
+        if cap_out is None and len(out_shape) >= 3:
+            cap_out = out_shape[2]
+        if (len(shape) < 3 or shape[:3] != head or src.dtype != dst.dtype or not src.is_contiguous()
+                or src.device != device or (dst is not src and (
+                    out_shape != (batch, heads, cap_out, *shape[3:]) or not dst.is_contiguous()
+                    or dst.device != device)) or (dst is src and cap_out != cap)):
+            raise ValueError(f"plane {i}: src and dst must be contiguous [batch][heads][cap][...] tensors like w, "
+                             "the destinations of one capacity")
         row = src.element_size()
-        for n in src.shape[3:]:
+        for n in shape[3:]:
             row *= n
-        arr[i] = _Plane(src.data_ptr(), dst.data_ptr(), row)
+        vals += (src.data_ptr(), dst.data_ptr(), row)
+    n_planes = len(vals) // 3
+    if cap_out is None:
+        cap_out = max(cap, int(budget))
+    arr = (ctypes.c_int64 * max(3, len(vals)))(*vals)  # rmm_cache_plane: two pointers and the row's bytes
     if lens_out is None:
         lens_out = torch.empty(batch, dtype=torch.int32, device=w.device)
     _i32_vec(lens_out, "lens_out", batch, w.device)
@@ -864,7 +871,7 @@ def cache_evict(w: torch.Tensor, lens: torch.Tensor, planes, budget: int, sink: 
     _i32_vec(idx_out, "idx_out", batch * heads * int(budget), w.device)
     ws = _ensure_ws(workspace, cache_evict_workspace_size(batch, heads, int(budget)), w.device)
     _check(lib().rmm_cache_evict(_ptr(w), _ptr(lens), batch, heads, cap, int(budget), int(sink), int(recent), arr,
-                                 len(pairs), cap_out, _ptr(lens_out), _ptr(idx_out), ctypes.c_void_p(ws.ptr),
+                                 n_planes, cap_out, _ptr(lens_out), _ptr(idx_out), ws.ptr,
                                  ws.nbytes, _stream(w)))
     return lens_out, idx_out, ws
 
