@@ -691,12 +691,15 @@ def attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.T
         raise ValueError("K and V disagree on shape, dtype or device")
     if out is None:
         out = torch.empty(T_q, h_q, d, dtype=out_dtype, device=Q.device)
+        o_ts, o_hs = h_q * d, d
     elif tuple(out.shape) != (T_q, h_q, d) or out.device != Q.device:
         raise ValueError("out must be [T_q][h_q][d] on Q's device")
-    _, _, _, o_ts, o_hs = _tokens(out, "out")
+    else:
+        _, _, _, o_ts, o_hs = _tokens(out, "out")
     if lse is None:
         lse = torch.empty(h_q, T_q, dtype=torch.float32, device=Q.device)
-    _f32_shape(lse, "lse", (h_q, T_q), Q.device)
+    else:
+        _f32_shape(lse, "lse", (h_q, T_q), Q.device)
     _check(lib().rmm_attn_prompt(_ptr(Q), q_ts, q_hs, _ptr(K), k_ts, k_hs, _ptr(V), v_ts, v_hs, _ptr(cu_q),
                                  _ptr(cu_k), n, T_q, T_k, h_q, h_kv, d, float(d ** -0.5 if scale is None else scale),
                                  int(causal), _dtype(Q), _ptr(out), o_ts, o_hs, _out_code(out.dtype), _ptr(lse),
@@ -779,7 +782,8 @@ def kv4_store(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, start: torch.Te
     _i32_vec(start, "start", cache.batch, K.device)
     if cu is not None:
         _i32_vec(cu, "cu", cache.batch + 1, K.device)
-    _f32_shape(w_new, "w_new", (h, T), K.device)
+    if w_new is not None:
+        _f32_shape(w_new, "w_new", (h, T), K.device)
     _check(lib().rmm_kv4_store(_ptr(K), k_ts, k_hs, _ptr(V), v_ts, v_hs, _dtype(K), _ptr(cu), _ptr(start),
                                cache.batch, T, h, d, cache.cap, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc),
                                _ptr(cache.vs), _ptr(w_new), _ptr(cache.w), _ptr(status), _stream(K)))
@@ -803,17 +807,22 @@ def kv4_attn(Q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, scale: float 
     if n != cache.batch or d != cache.d or Q.device != cache.kc.device:
         raise ValueError("Q and the cache disagree on batch, d or device")
     _i32_vec(lens, "lens", n, Q.device)
-    for name, t in (("w_in", w_in), ("w_out", w_out)):
-        _f32_shape(t, name, (n, cache.heads, cache.cap), Q.device)
+    if w_in is not None:
+        _f32_shape(w_in, "w_in", (n, cache.heads, cache.cap), Q.device)
+    if w_out is not None:
+        _f32_shape(w_out, "w_out", (n, cache.heads, cache.cap), Q.device)
     ws = _ensure_ws(workspace, kv4_attn_workspace_size(n, h_q, cache.heads, d, cache.cap, w_out is not None), Q.device)
     if out is None:
         out = torch.empty(n, h_q, d, dtype=out_dtype, device=Q.device)
+        o_ss, o_hs = h_q * d, d
     elif tuple(out.shape) != (n, h_q, d) or out.device != Q.device:
         raise ValueError("out must be [batch][h_q][d] on Q's device")
-    _, _, _, o_ss, o_hs = _tokens(out, "out")
+    else:
+        _, _, _, o_ss, o_hs = _tokens(out, "out")
     if lse is None:
         lse = torch.empty(n, h_q, dtype=torch.float32, device=Q.device)
-    _f32_shape(lse, "lse", (n, h_q), Q.device)
+    else:
+        _f32_shape(lse, "lse", (n, h_q), Q.device)
     _check(lib().rmm_kv4_attn(_ptr(Q), q_ss, q_hs, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs),
                               _ptr(lens), n, h_q, cache.heads, d, cache.cap,
                               float(d ** -0.5 if scale is None else scale), _dtype(Q), _ptr(out), o_ss, o_hs,
