@@ -38,7 +38,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128;  // rows of a tile, keys of a key tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers per thread: 168 at launch (64512 for 384 threads); the eight softmax
+// warps, with a row of S and their row's state, take what the other four give back.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "registers of the block");
 constexpr float kRescale = 8.0f;  // log2 of the growth of P that is let through unscaled
 
 struct TcArgs {
@@ -129,6 +133,19 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
   return as_f32x2(r);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   uint64_t r;
@@ -232,6 +249,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
     const int32_t n = max(nk[0], nk[1]);
 
+    if (warp >= 8) {
+    fewer_registers<kOtherRegs>();
     if (warp == 9) {
       // ---------------------------------------------------------- TMA (one lane)
       if (lane == 0) {
@@ -360,7 +379,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         mbar_wait_bounded(drain, 0, limit, never_v);
       }
       __syncwarp();
+    }
     } else {
+      more_registers<kSoftmaxRegs>();
       // ---------------------------------------------------------- softmax, one row per thread
       const int t = warp >> 2;
       const int r = (warp & 3) * 32 + lane;
@@ -393,11 +414,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         float mx[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          mx[x] = __uint_as_float(s[x][0]);
+          mx[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[x] = fmaxf(mx[x], __uint_as_float(s[x][e]));
+          for (int e = 2; e < 32; e += 2) mx[x] = max3(mx[x], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
         }
-        const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(fmaxf(mx[2], mx[3]), m));
+        const float m2 = fmaxf(max3(mx[0], mx[1], mx[2]), fmaxf(mx[3], m));
         // (m2 - m)·c, a first maximum counting as growth
         if (__any_sync(0xffffffffu, m2 > m && !(fmaf(m2, c, nm) <= kRescale && m > -INFINITY))) {
           const float nm2 = m2 > -INFINITY ? -m2 * c : 0.f;
@@ -417,20 +438,24 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           m = m2;
           nm = nm2;
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(nm, nm);
+        float2 sum[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sum[x] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[x][2 * e]), c, nm));
-            const float p1 = ex2(fmaf(__uint_as_float(s[x][2 * e + 1]), c, nm));
-            sum[e & 3] += p0 + p1;
-            pk[e] = pack_bf16x2(p0, p1);
+            const float2 y = fma2(make_float2(__uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1])), c2, nm2);
+            const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+            sum[e & 3] = add2(sum[e & 3], pe);
+            pk[e] = pack_bf16x2(pe.x, pe.y);
           }
           tmem_st_32x32b_x16(tS + 16 * x, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 sums = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += sums.x + sums.y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
