@@ -43,6 +43,7 @@ constexpr int kThreads = 384;
 // warps, with a row of S and their row's state, take what the other four give back.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "registers of the block");
+constexpr int kPromptPoly = 0, kWeightsPoly = 0;  // of 8 pairs of exponentials, those by polynomial
 constexpr float kRescale = 8.0f;  // log2 of the growth of P that is let through unscaled
 
 struct TcArgs {
@@ -153,6 +154,40 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return as_f32x2(r);
 }
 
+// 2^x for two x of at most 127 with multiply-adds alone, for the share of a
+// row's exponentials that the special-function units (16 a cycle per SM, the
+// rate the tensor cores need them at) have no time for. x = n + f, n the
+// nearest integer (from the low bits of x + 1.5·2^23), 2^f by a polynomial of
+// degree 5 with p(0) = 1, fitted for the least relative error on [-1/2, 1/2]
+// (1.6e-7, rounding included), n added to its exponent. Below -127 the result
+// is 0; a NaN comes out as NaN or as 2^128 - 2^104, which no sum of
+// probabilities comes near: kNoSum tells both.
+constexpr float kNoSum = 0x1p100f;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  auto both = [](float v) { return make_float2(v, v); };
+  x = make_float2(max_nan(x.x, -127.f), max_nan(x.y, -127.f));
+  const float2 t = add2(x, both(12582912.f));
+  const float2 f = fma2(add2(t, both(-12582912.f)), both(-1.f), x);
+  float2 p = fma2(both(0.001326472731307149f), f, both(0.009671512991189957f));
+  p = fma2(p, f, both(0.05550733581185341f));
+  p = fma2(p, f, both(0.24022242426872253f));
+  p = fma2(p, f, both(0.6931470036506653f));
+  p = fma2(p, f, both(1.f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+// Pairs i of every 8 for which the polynomial is taken.
+template <int OF8>
+__device__ __forceinline__ float2 ex2_pair(float2 x, int i) {
+  const bool poly = (i % 8) * OF8 / 8 != (i % 8 + 1) * OF8 / 8;
+  return poly ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
+}
+
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t* status) {
   *abort_flag = 1;
   status_or(status, RMM_TIMEOUT_BIT);
@@ -162,6 +197,20 @@ __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t* 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit, const volatile int* abort) {
   const bool ok = mbar_wait_bounded(bar, parity, limit, abort);
   return __all_sync(0xffffffffu, ok);
+}
+
+// D = A·Bᵀ over d: A's rows 128 by 64-channel boxes of 128 rows, B's of BROWS
+// rows, both as TMA wrote them. ksteps: 16 channels each, up to DP / 16.
+template <int DP, int BROWS>
+__device__ __forceinline__ void issue_product(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, int ksteps) {
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk) {
+    if (kk == 0)
+      umma_bf16_lo<false>(d_tmem, a_lo, b_lo, idesc);
+    else if (kk < ksteps)
+      umma_bf16_lo<true>(d_tmem, a_lo + (kk >> 2) * (kRows * 128 >> 4) + (kk & 3) * 2,
+                         b_lo + (kk >> 2) * (BROWS * 128 >> 4) + (kk & 3) * 2, idesc);
+  }
 }
 
 template <int DP>
@@ -299,6 +348,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const uint32_t id_s = umma_idesc_bf16_f32(kRows, kRows, false);
       const uint32_t id_o = umma_idesc_bf16_f32(kRows, dn, true);
       const int ksteps = int(dn / 16);
+      const uint32_t desc_q = umma_desc_lo(smem_addr(sQ)), desc_kv = umma_desc_lo(smem_addr(sKV));
+      const uint32_t desc_v = umma_desc_lo(smem_addr(sKV), Cfg::BOX);  // channels contiguous, 64 to a box
       bool ok = true;
       uint32_t p_par[2] = {0u, 0u};
       auto ring = [&](int32_t i, uint32_t& stage, uint32_t& par) {
@@ -307,21 +358,18 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       };
       auto issue_s = [&](int t, uint32_t stage) {
         if (lane == 0) {
-          const uint32_t q = smem_addr(sQ + t * Cfg::TILE), k = smem_addr(sKV + stage * Cfg::TILE);
-          for (int kk = 0; kk < ksteps; ++kk) {
-            const uint32_t o = uint32_t(kk >> 2) * Cfg::BOX + uint32_t(kk & 3) * 32;
-            umma_bf16<1>(tmem + t * 128, umma_desc_k_sw128(q + o), umma_desc_k_sw128(k + o), id_s, kk != 0);
-          }
+          issue_product<DP, kRows>(tmem + t * 128, desc_q + t * (Cfg::TILE >> 4), desc_kv + stage * (Cfg::TILE >> 4),
+                                   id_s, ksteps);
           umma_commit<1>(smem_addr(&s_full[t]));
         }
       };
       auto issue_o = [&](int t, uint32_t stage, int32_t j) {
         if (lane == 0) {
-          const uint32_t v = smem_addr(sKV + stage * Cfg::TILE);
+          const uint32_t v = desc_v + stage * (Cfg::TILE >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, umma_desc_mn_sw128(v + kk * 2048, Cfg::BOX),
-                         id_o, j != 0 || kk != 0);
+            umma_bf16_ts_lo(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, v + kk * (2048 >> 4), id_o,
+                            kk != 0 ? 1u : uint32_t(j));
           if (j == nk[t] - 1) umma_commit<1>(smem_addr(&o_full[t]));
         }
       };
@@ -448,7 +496,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = fma2(make_float2(__uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1])), c2, nm2);
-            const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+            const float2 pe = ex2_pair<kPromptPoly>(y, e);
             sum[e & 3] = add2(sum[e & 3], pe);
             pk[e] = pack_bf16x2(pe.x, pe.y);
           }
@@ -469,7 +517,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int64_t tok = int64_t(w.s.q0) + q, hq = int64_t(h) * p.g + r % p.g;
         const bool any = lim > 0 && nk[t] > 0;
         if (row_ok) {
-          if (any && !(l > 0.f && l < INFINITY)) status_or(a.status, RMM_NONFINITE_BIT);
+          if (any && !(l > 0.f && l < kNoSum)) {
+            status_or(a.status, RMM_NONFINITE_BIT);
+            l = NAN;
+          }
           if (a.lse) a.lse[hq * a.T_q + tok] = any ? (log2f(l) - nm) * kLn2 : -INFINITY;
         }
         const float inv = any ? 1.0f / l : 0.f;
@@ -668,6 +719,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
     } else if (warp == 8) {
       const uint32_t id_s = umma_idesc_bf16_f32(kRows, kRows, false);
       const int ksteps = int((a.d + 15) / 16);
+      const uint32_t desc_k = umma_desc_lo(smem_addr(sK)), desc_q = umma_desc_lo(smem_addr(sQ));
       bool ok = true;
       uint32_t stage = 0, phase = 0, par[2] = {0u, 0u}, seen[2] = {0u, 0u};
       for (int32_t i = begin; ok && i < n_qt; i += step) {
@@ -687,12 +739,8 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
           }
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t q = smem_addr(sQ + stage * Cfg::TILE), k = smem_addr(sK + t * Cfg::TILE);
-            for (int kk = 0; kk < ksteps; ++kk) {
-              const uint32_t o = uint32_t(kk >> 2) * Cfg::BOX + uint32_t(kk & 3) * 32;
-              umma_bf16<1>(tmem + (t * 2 + buf) * 128, umma_desc_k_sw128(k + o), umma_desc_k_sw128(q + o), id_s,
-                           kk != 0);
-            }
+            issue_product<DP, kRows>(tmem + (t * 2 + buf) * 128, desc_k + t * (Cfg::TILE >> 4),
+                                     desc_q + stage * (Cfg::TILE >> 4), id_s, ksteps);
             umma_commit<1>(smem_addr(&s_full[t * 2 + buf]));
           }
         }
@@ -710,23 +758,34 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
       }
       __syncwarp();
     } else if (warp == 10) {
+      // a tile's values are read before the one before it is handed over
+      constexpr int N = 4;
+      const float* src[N];
+      float v[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int32_t c = 32 * e + lane;
+        src[e] = a.lse + int64_t(h * p.g + c % p.g) * a.T_q + w.s.q0 + c / p.g;
+      }
+      auto read = [&](int32_t i) {
+        const int32_t q0 = i * p.nq_tile, live = min(p.nq_tile, S_q - q0) * p.g;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = 32 * e + lane < live ? src[e][q0] : 0.f;
+      };
+      read(begin);
       bool ok = true;
       uint32_t r = 0, phase = 0;
       for (int32_t i = begin; i < n_qt; i += step) {
-        const int32_t q0 = i * p.nq_tile;
-        const int32_t live = min(p.nq_tile, S_q - q0) * p.g;
-        float v[4];
+        float nl[N];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int32_t c = 32 * e + lane;
-          v[e] = c < live ? a.lse[int64_t(h * p.g + c % p.g) * a.T_q + w.s.q0 + q0 + c / p.g] : 0.f;
-        }
+        for (int e = 0; e < N; ++e) nl[e] = -v[e] * kLog2e;
+        read(i + step);
         if (!warp_wait(&l_empty[r], phase ^ 1u, limit, abort_v)) {
           ok = false;
           break;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) lse_sh[r * kRows + 32 * e + lane] = -v[e] * kLog2e;
+        for (int e = 0; e < N; ++e) lse_sh[r * kRows + 32 * e + lane] = nl[e];
         __syncwarp();
         if (lane == 0) mbar_arrive(&l_full[r]);
         if (++r == kLseRing) {
@@ -793,7 +852,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                     if (col + 1 < lo || col + 1 >= hi) y[z].y = -INFINITY;
                   }
                   float2& sum = part[((e >> 1) + z) & 3];
-                  sum = add2(sum, make_float2(ex2(y[z].x), ex2(y[z].y)));
+                  sum = add2(sum, ex2_pair<kWeightsPoly>(y[z], (e >> 1) + z));
                 }
               }
             };
@@ -836,7 +895,10 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
       } else {
         for (uint32_t r = 0; r < p.split; ++r) x += ld_cluster_f32(mapa_shared(smem_addr(sum_sh + i), r));
       }
-      if (!isfinite(x)) status_or(a.status, RMM_NONFINITE_BIT);
+      if (!(x < kNoSum)) {
+        status_or(a.status, RMM_NONFINITE_BIT);
+        x = NAN;
+      }
       const int64_t at = int64_t(h) * a.T_k + w.s.k0 + k;
       a.w_out[at] = a.w_in ? a.w_in[at] + x : x;
     }
@@ -933,7 +995,7 @@ cudaError_t launch_weights(TcArgs p, cudaStream_t st, const char** why) {
   // enough CTAs to even out the units' different lengths over 148 SMs, but at least 4 query tiles each
   const int64_t q_tiles = (a.T_q / std::max<int64_t>(a.n_seq, 1)) / p.nq_tile;
   p.split = 1;
-  while (p.split < 8 && units * p.split < 4 * 148 && q_tiles >= 8 * int64_t(p.split)) p.split *= 2;
+  while (p.split < 8 && units * p.split < 400 && q_tiles >= 8 * int64_t(p.split)) p.split *= 2;
   return launch_pdl(attn_key_weights_kernel<DP>, dim3(unsigned(units * p.split)), dim3(kWtThreads), Cfg::SMEM, st,
                     p.split > 1 ? dim3(p.split, 1, 1) : dim3(0, 0, 0), tmQ, tmK, p);
 }

@@ -232,18 +232,6 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] · B[smem desc]: A's rows on TMEM lanes, two bf16 per
-// 32-bit column along the contraction.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Arrive once on the mbarrier at cluster address `bar` (this CTA's or the
 // peer's) when every tcgen05 op this thread issued so far is done.
 template <int CG>
@@ -321,6 +309,37 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_byte_addr, 
   d |= uint64_t(1) << 46;
   d |= uint64_t(2) << 61;
   return d;
+}
+
+// The same two descriptors as halves: a low word that may be advanced by plain
+// additions of bytes >> 4 (a tile lies below 2^18), and the high word every
+// 128-byte-swizzled tile shares. An issuing thread that builds whole 64-bit
+// descriptors for each product of a short K loop takes longer than the product.
+constexpr uint32_t kUmmaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t smem_byte_addr, uint32_t leading_bytes = 16) {
+  return ((smem_byte_addr >> 4) & 0x3FFFu) | ((leading_bytes >> 4) << 16);
+}
+template <bool ACC>
+__device__ __forceinline__ void umma_bf16_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(int(ACC)), "n"(kUmmaDescHi)
+      : "memory");
+}
+// A's rows on TMEM lanes, two bf16 per 32-bit column along the contraction.
+__device__ __forceinline__ void umma_bf16_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kUmmaDescHi)
+      : "memory");
 }
 
 // Instruction descriptor, kind::f16: f32 accumulator (bits 4-5 = 1), A and B
