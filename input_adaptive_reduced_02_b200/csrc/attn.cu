@@ -9,19 +9,24 @@
 // idle). So the g heads read their keys and values once, and a causal tile
 // spans few queries.
 //
-// Attention, per CTA two such tiles and one key head:
+// Attention, per CTA two such tiles t and one key head:
 //   warps 0-3, 4-7  one row per thread: S from TMEM, running maximum and sum
 //                   in log2 units, P as bf16 back to TMEM over S
-//   warp 8          one lane issues tcgen05.mma: S_t = Q_t·Kᵀ (both operands
-//                   in shared memory) and O_t += P_t·V (P in TMEM); while one
+//   warps 8, 9      tile 0 and 1: tcgen05.mma, S_t = Q_t·Kᵀ (both operands in
+//                   shared memory) and O_t += P_t·V (P in TMEM); while one
 //                   tile's softmax runs, the other tile's products do
-//   warp 9          TMA: Q once, then K and V tiles of 128 keys through one ring
+//   warp 10         TMA: Q once, then K and V tiles of 128 keys through one
+//                   ring; zeroes the value rows past the sequence's end
 // TMEM: S_0, S_1, O_0, O_1 of 128 columns each. O is rescaled in TMEM by the
 // softmax warps themselves, and only when a row's maximum grew by more than
 // 2^8 in the exponential's argument: P then stays below 256, which bf16 and
 // the f32 sums hold as well as values below 1. The barrier that hands S_t(j)
-// over tracks every product issued before it, P_t·V of tile j-1 among them,
-// so O needs no barrier of its own.
+// over tracks every product issued before it, P_t·V of tile j-1 among them, so O
+// needs no barrier of its own.
+// A tile's softmax and its products take turns, and that chain bounds the
+// kernel: per 128 keys about 2000 cycles of softmax (16 exponentials a cycle
+// per SM: 1024 for 128 x 128) and 1400 of P·V (512), S (800: both operands
+// from shared memory come at 82 of 128 bytes a cycle) and handovers.
 // Every wait is bounded (rmm_set_wait_limit_ns) as in gemm_tc.cu.
 #include <cudaTypedefs.h>
 
@@ -204,13 +209,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
 template <int DP, int BROWS>
 __device__ __forceinline__ void issue_product(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, int ksteps) {
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) {
-    if (kk == 0)
-      umma_bf16_lo<false>(d_tmem, a_lo, b_lo, idesc);
-    else if (kk < ksteps)
-      umma_bf16_lo<true>(d_tmem, a_lo + (kk >> 2) * (kRows * 128 >> 4) + (kk & 3) * 2,
-                         b_lo + (kk >> 2) * (BROWS * 128 >> 4) + (kk & 3) * 2, idesc);
-  }
+  for (int kk = 0; kk < DP / 16; ++kk)
+    if (kk < ksteps)
+      umma_bf16_warp(d_tmem, a_lo + (kk >> 2) * (kRows * 128 >> 4) + (kk & 3) * 2,
+                     b_lo + (kk >> 2) * (BROWS * 128 >> 4) + (kk & 3) * 2, idesc, kk != 0);
 }
 
 template <int DP>
@@ -239,30 +241,33 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint64_t* s_full = q_full + 2;        // [2] S_t ready (and O_t up to the previous key tile)
   uint64_t* p_full = s_full + 2;        // [2] P_t written, O_t rescaled
   uint64_t* o_full = p_full + 2;        // [2] O_t complete
-  uint64_t* drain = o_full + 2;
-  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* v_zeroed = o_full + 2;
+  uint64_t* drain = v_zeroed + 1;       // [2]
+  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(drain + 2);
   int* abort_sh = reinterpret_cast<int*>(tmem_base_sh + 1);
   int* never_sh = abort_sh + 1;  // stays 0: waits that must not be cut short
+  static_assert((2 * STAGES + 11) * 8 + 3 * 4 <= 256, "barrier area");
 
   const AttnArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
+      mbar_init(&drain[t], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(v_zeroed, 1);
     *abort_sh = 0;
     *never_sh = 0;
     fence_mbar_init();
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == 10 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -300,11 +305,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
     if (warp >= 8) {
     fewer_registers<kOtherRegs>();
-    if (warp == 9) {
+    if (warp == 10) {
       // ---------------------------------------------------------- TMA (one lane)
+      bool ok = true;
+      uint32_t issued = 0, issued_par = 0;
       if (lane == 0) {
-        bool ok = true;
-        uint32_t issued = 0, issued_par = 0;
         for (int t = 0; t < 2; ++t) {
           if (nk[t] == 0) continue;
           mbar_arrive_expect_tx(&q_full[t], uint32_t(Cfg::BOXES * p.row_bytes));
@@ -332,6 +337,24 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
         if (!ok) raise_abort(abort_v, a.status);
+      }
+      // Value rows past the sequence's end: their probabilities are 0, but their memory may hold NaN.
+      ok = __shfl_sync(0xffffffffu, int(ok), 0);
+      if (ok && n > 0 && n * kRows > S_k) {
+        const uint32_t st = uint32_t(2 * n - 1) % STAGES, par = (uint32_t(2 * n - 1) / STAGES) & 1u;
+        if (warp_wait(&full[st], par, limit, abort_v)) {
+          for (int32_t r = S_k - (n - 1) * kRows; r < kRows; ++r)
+            for (int c = lane; c < Cfg::BOXES * 8; c += 32)
+              *reinterpret_cast<uint4*>(sKV + st * Cfg::TILE + (c >> 3) * Cfg::BOX + r * 128 + (c & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_zeroed);
+        } else if (lane == 0) {
+          raise_abort(abort_v, a.status);
+        }
+      }
+      if (lane == 0) {
         // no load may still be writing shared memory when the CTA exits
         for (int t = 0; t < 2; ++t)
           if (nk[t] > 0) mbar_wait_bounded(&q_full[t], 0, limit, never_v);
@@ -339,93 +362,70 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (issued & (1u << s)) mbar_wait_bounded(&full[s], (issued_par >> s) & 1u, limit, never_v);
       }
       __syncwarp();
-    } else if (warp == 8) {
-      // ---------------------------------------------------------- MMA
-      // The whole warp waits (it also zeroes the value rows past the
-      // sequence's end, whose probabilities are 0 but whose memory may hold
-      // NaN); lane 0 issues.
+    } else if (warp < 10) {
+      // ---------------------------------------------------------- MMA of tile t
+      const int t = warp - 8;
+      const int32_t nt = t == 0 ? nk[0] : nk[1];
       const uint32_t dn = uint32_t((a.d + 15) / 16 * 16);
       const uint32_t id_s = umma_idesc_bf16_f32(kRows, kRows, false);
       const uint32_t id_o = umma_idesc_bf16_f32(kRows, dn, true);
       const int ksteps = int(dn / 16);
-      const uint32_t desc_q = umma_desc_lo(smem_addr(sQ)), desc_kv = umma_desc_lo(smem_addr(sKV));
+      const uint32_t desc_q = umma_desc_lo(smem_addr(sQ)) + t * (Cfg::TILE >> 4);
+      const uint32_t desc_k = umma_desc_lo(smem_addr(sKV));
       const uint32_t desc_v = umma_desc_lo(smem_addr(sKV), Cfg::BOX);  // channels contiguous, 64 to a box
+      const uint32_t tS = tmem + t * 128, tO = tS + 256;
       bool ok = true;
-      uint32_t p_par[2] = {0u, 0u};
-      auto ring = [&](int32_t i, uint32_t& stage, uint32_t& par) {
-        stage = uint32_t(i) % STAGES;
-        par = (uint32_t(i) / STAGES) & 1u;
-      };
-      auto issue_s = [&](int t, uint32_t stage) {
-        if (lane == 0) {
-          issue_product<DP, kRows>(tmem + t * 128, desc_q + t * (Cfg::TILE >> 4), desc_kv + stage * (Cfg::TILE >> 4),
-                                   id_s, ksteps);
-          umma_commit<1>(smem_addr(&s_full[t]));
+      uint32_t ring = 0, phase = 0;  // of the next K or V tile
+      auto next = [&] {
+        if (++ring == STAGES) {
+          ring = 0;
+          phase ^= 1u;
         }
       };
-      auto issue_o = [&](int t, uint32_t stage, int32_t j) {
-        if (lane == 0) {
-          const uint32_t v = desc_v + stage * (Cfg::TILE >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts_lo(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, v + kk * (2048 >> 4), id_o,
-                            kk != 0 ? 1u : uint32_t(j));
-          if (j == nk[t] - 1) umma_commit<1>(smem_addr(&o_full[t]));
-        }
+      auto issue_s = [&](uint32_t stage) {
+        issue_product<DP, kRows>(tS, desc_q, desc_k + stage * (Cfg::TILE >> 4), id_s, ksteps);
+        umma_commit_warp(&s_full[t]);
       };
-      uint32_t st, par;
       if (n > 0) {
-        ring(0, st, par);
-        ok = warp_wait(&full[st], par, limit, abort_v);
-        for (int t = 0; ok && t < 2; ++t) {
-          if (nk[t] == 0) continue;
-          ok = warp_wait(&q_full[t], 0, limit, abort_v);
-          if (ok) {
-            tc_fence_after();
-            issue_s(t, st);
-          }
+        ok = (nt == 0 || warp_wait(&q_full[t], 0, limit, abort_v)) && warp_wait(&full[0], 0, limit, abort_v);
+        if (ok) {
+          tc_fence_after();
+          if (nt > 0) issue_s(0);
+          umma_commit_warp(&empty[0]);
+          next();
         }
-        if (ok && lane == 0) umma_commit<1>(smem_addr(&empty[st]));
       }
       for (int32_t j = 0; ok && j < n; ++j) {
-        uint32_t vst, vpar, kst = 0, kpar = 0;
-        ring(2 * j + 1, vst, vpar);
-        ok = warp_wait(&full[vst], vpar, limit, abort_v);
-        if (!ok) break;
-        const int32_t past = (j + 1) * kRows - S_k;  // rows of this tile past the sequence
-        if (past > 0) {
-          for (int32_t r = kRows - past; r < kRows; ++r)
-            for (int c = lane; c < Cfg::BOXES * 8; c += 32)
-              *reinterpret_cast<uint4*>(sKV + vst * Cfg::TILE + (c >> 3) * Cfg::BOX + r * 128 + (c & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+        // what the products need besides P, which comes last
+        const uint32_t vst = ring;
+        ok = warp_wait(&full[ring], phase, limit, abort_v);
+        if (ok && j == n - 1 && n * kRows > S_k) ok = warp_wait(v_zeroed, 0, limit, abort_v);
+        next();
+        const uint32_t kst = ring;
         const bool more = j + 1 < n;
-        for (int t = 0; ok && t < 2; ++t) {
-          if (j < nk[t]) {
-            ok = warp_wait(&p_full[t], p_par[t], limit, abort_v);
-            if (!ok) break;
-            p_par[t] ^= 1u;
-            tc_fence_after();
-            issue_o(t, vst, j);
-          }
-          if (t == 0 && more) {
-            ring(2 * j + 2, kst, kpar);
-            ok = warp_wait(&full[kst], kpar, limit, abort_v);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (t == 1 && lane == 0) umma_commit<1>(smem_addr(&empty[vst]));
-          if (j + 1 < nk[t]) issue_s(t, kst);
-          if (t == 1 && more && lane == 0) umma_commit<1>(smem_addr(&empty[kst]));
+        if (ok && more) ok = warp_wait(&full[ring], phase, limit, abort_v);
+        if (ok && j < nt) ok = warp_wait(&p_full[t], uint32_t(j) & 1u, limit, abort_v);
+        if (!ok) break;
+        if (j < nt) {
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_ts_warp(tO, tS + kk * 8, desc_v + vst * (Cfg::TILE >> 4) + kk * (2048 >> 4), id_o,
+                              kk != 0 ? 1u : uint32_t(j));
+          if (j + 1 < nt)
+            issue_s(kst);
+          else
+            umma_commit_warp(&o_full[t]);
+        }
+        umma_commit_warp(&empty[vst]);
+        if (more) {
+          umma_commit_warp(&empty[kst]);
+          next();
         }
       }
-      if (lane == 0) {
-        if (!ok) raise_abort(abort_v, a.status);
-        umma_commit<1>(smem_addr(drain));  // every product done before tensor memory is freed
-        mbar_wait_bounded(drain, 0, limit, never_v);
-      }
+      if (!ok && lane == 0) raise_abort(abort_v, a.status);
+      umma_commit_warp(&drain[t]);  // every product done before tensor memory is freed
+      mbar_wait_bounded(&drain[t], 0, limit, never_v);
       __syncwarp();
     }
     } else {
@@ -620,7 +620,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
   static_assert((2 * STAGES + 2 * kLseRing + 11) * 8 + 12 <= 256, "barrier area");
 
   const AttnArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x % p.split;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -738,24 +738,20 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             par[t] ^= 1u << buf;
           }
           tc_fence_after();
-          if (lane == 0) {
-            issue_product<DP, kRows>(tmem + (t * 2 + buf) * 128, desc_k + t * (Cfg::TILE >> 4),
-                                     desc_q + stage * (Cfg::TILE >> 4), id_s, ksteps);
-            umma_commit<1>(smem_addr(&s_full[t * 2 + buf]));
-          }
+          issue_product<DP, kRows>(tmem + (t * 2 + buf) * 128, desc_k + t * (Cfg::TILE >> 4),
+                                   desc_q + stage * (Cfg::TILE >> 4), id_s, ksteps);
+          umma_commit_warp(&s_full[t * 2 + buf]);
         }
         if (!ok) break;
-        if (lane == 0) umma_commit<1>(smem_addr(&empty[stage]));
+        umma_commit_warp(&empty[stage]);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (lane == 0) {
-        if (!ok) raise_abort(abort_v, a.status);
-        umma_commit<1>(smem_addr(drain));
-        mbar_wait_bounded(drain, 0, limit, never_v);
-      }
+      if (!ok && lane == 0) raise_abort(abort_v, a.status);
+      umma_commit_warp(drain);
+      mbar_wait_bounded(drain, 0, limit, never_v);
       __syncwarp();
     } else if (warp == 10) {
       // a tile's values are read before the one before it is handed over

@@ -712,9 +712,11 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
 }
 
 // Joins the parts of each item. Blocks [0, batch·h_q): O and the log-sum-exp of
-// one head. The rest, w_out = w_in + the group's probabilities, 512 tokens each.
-constexpr int kJoinThreads = 128;
-constexpr int kJoinTokens = 512;
+// one head. The rest, w_out = w_in + the group's probabilities, kJoinTokens
+// each; their scores are on the way while the parts' sums are joined.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinEach = 4;  // tokens of a thread
+constexpr int kJoinTokens = kJoinThreads * kJoinEach;
 
 // The slots of an item's parts: [first, last].
 struct Parts {
@@ -742,6 +744,8 @@ __device__ __forceinline__ float2 join_ml(const Kv4Dev& p, Parts s, int32_t head
   return make_float2(m, l);
 }
 
+// GV: query heads per key head, where that is 4 or 8 (16-byte loads); else 0.
+template <int GV>
 __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4Dev p, int64_t o_blocks) {
   extern __shared__ float lse2[];  // [h_q / h_kv]
   pdl_trigger();
@@ -753,7 +757,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
     const int64_t b = blockIdx.x / a.h_q, hq = blockIdx.x % a.h_q;
     const int32_t len = seq_len(a, b);
     const int32_t hg = int32_t(hq % gq), head = hg % p.chunk_heads;
-    const Parts parts = item_parts(p, b, hq / gq * p.chunks + hg / p.chunk_heads, len);
+    const Parts parts = item_parts(p, b, int32_t(hq / gq) * p.chunks + hg / p.chunk_heads, len);
     float2 g = make_float2(-INFINITY, 0.f);
     if (len > 0) g = join_ml(p, parts, head, lane);
     if (tid == 0) {
@@ -786,18 +790,37 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
   const int32_t len = seq_len(a, b);
   const int32_t t0 = int32_t(i % pieces) * kJoinTokens;
   if (t0 >= len) return;
+  float x[kJoinEach][GV > 0 ? GV : 1], w[kJoinEach];
+#pragma unroll
+  for (int e = 0; e < kJoinEach; ++e) {
+    const int32_t t = min(t0 + e * kJoinThreads + tid, len - 1);
+    const int64_t at = item * a.cap + t;
+#pragma unroll
+    for (int v = 0; v < GV / 4; ++v) {
+      const float4 u = reinterpret_cast<const float4*>(p.scores + at * GV)[v];
+      x[e][4 * v] = u.x, x[e][4 * v + 1] = u.y, x[e][4 * v + 2] = u.z, x[e][4 * v + 3] = u.w;
+    }
+    w[e] = a.w_in ? a.w_in[at] : 0.f;
+  }
   for (int g = warp; g < gq; g += kJoinThreads / 32) {
-    const Parts parts = item_parts(p, b, h * p.chunks + g / p.chunk_heads, len);
+    const Parts parts = item_parts(p, b, int32_t(h) * p.chunks + g / p.chunk_heads, len);
     const float2 ml = join_ml(p, parts, g % p.chunk_heads, lane);
     if (lane == 0) lse2[g] = ml.x + log2f(ml.y);
   }
   __syncthreads();
-  const int32_t t1 = min(len, t0 + kJoinTokens);
-  for (int32_t t = t0 + tid; t < t1; t += kJoinThreads) {
-    float s = 0.f;
-    for (int g = 0; g < gq; ++g) s += exp2f(p.scores[(item * a.cap + t) * gq + g] - lse2[g]);
+#pragma unroll
+  for (int e = 0; e < kJoinEach; ++e) {
+    const int32_t t = t0 + e * kJoinThreads + tid;
+    if (t >= len) break;
     const int64_t at = item * a.cap + t;
-    a.w_out[at] = a.w_in ? a.w_in[at] + s : s;
+    float s = 0.f;
+    if constexpr (GV > 0) {
+#pragma unroll
+      for (int g = 0; g < GV; ++g) s += exp2f(x[e][g] - lse2[g]);
+    } else {
+      for (int g = 0; g < gq; ++g) s += exp2f(p.scores[at * gq + g] - lse2[g]);
+    }
+    a.w_out[at] = w[e] + s;
   }
 }
 
@@ -884,8 +907,11 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t o_blocks = a.batch * a.h_q;
   const int64_t w_blocks = a.w_out ? a.batch * a.h_kv * ((a.cap + kJoinTokens - 1) / kJoinTokens) : 0;
-  return launch_pdl(kv4_attn_join_kernel, dim3(unsigned(o_blocks + w_blocks)), dim3(kJoinThreads),
-                    size_t(a.h_q / a.h_kv) * 4, st, dim3(0, 0, 0), p, o_blocks);
+  const int64_t group = a.h_q / a.h_kv;
+  const dim3 grid(unsigned(o_blocks + w_blocks)), block(kJoinThreads), none(0, 0, 0);
+  if (group == 4) return launch_pdl(kv4_attn_join_kernel<4>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
+  if (group == 8) return launch_pdl(kv4_attn_join_kernel<8>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
+  return launch_pdl(kv4_attn_join_kernel<0>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
 }
 
 }  // namespace rmm
