@@ -48,7 +48,6 @@ constexpr int kThreads = 384;
 // warps, with a row of S and their row's state, take what the other four give back.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(8 * kSoftmaxRegs + 4 * kOtherRegs <= 12 * 168, "registers of the block");
-constexpr int kPromptPoly = 0, kWeightsPoly = 0;  // of 8 pairs of exponentials, those by polynomial
 constexpr float kRescale = 8.0f;  // log2 of the growth of P that is let through unscaled
 
 struct TcArgs {
@@ -157,40 +156,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
   return as_f32x2(r);
-}
-
-// 2^x for two x of at most 127 with multiply-adds alone, for the share of a
-// row's exponentials that the special-function units (16 a cycle per SM, the
-// rate the tensor cores need them at) have no time for. x = n + f, n the
-// nearest integer (from the low bits of x + 1.5·2^23), 2^f by a polynomial of
-// degree 5 with p(0) = 1, fitted for the least relative error on [-1/2, 1/2]
-// (1.6e-7, rounding included), n added to its exponent. Below -127 the result
-// is 0; a NaN comes out as NaN or as 2^128 - 2^104, which no sum of
-// probabilities comes near: kNoSum tells both.
-constexpr float kNoSum = 0x1p100f;
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 ex2_poly(float2 x) {
-  auto both = [](float v) { return make_float2(v, v); };
-  x = make_float2(max_nan(x.x, -127.f), max_nan(x.y, -127.f));
-  const float2 t = add2(x, both(12582912.f));
-  const float2 f = fma2(add2(t, both(-12582912.f)), both(-1.f), x);
-  float2 p = fma2(both(0.001326472731307149f), f, both(0.009671512991189957f));
-  p = fma2(p, f, both(0.05550733581185341f));
-  p = fma2(p, f, both(0.24022242426872253f));
-  p = fma2(p, f, both(0.6931470036506653f));
-  p = fma2(p, f, both(1.f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
-// Pairs i of every 8 for which the polynomial is taken.
-template <int OF8>
-__device__ __forceinline__ float2 ex2_pair(float2 x, int i) {
-  const bool poly = (i % 8) * OF8 / 8 != (i % 8 + 1) * OF8 / 8;
-  return poly ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
 }
 
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t* status) {
@@ -474,13 +439,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const float f = m > -INFINITY ? ex2(nm2 - nm) : 1.f;
             l *= f;
 #pragma unroll
-            for (int x = 0; x < DP / 32; ++x) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tO + 32 * x, o);
-              tmem_ld_wait();
+            for (int x = 0; x < DP / 16; ++x) {  // few columns at a time: S is in registers too
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(tO + 16 * x, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x32(tO + 32 * x, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x16(tO + 16 * x, o);
             }
           }
           m = m2;
@@ -496,7 +460,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = fma2(make_float2(__uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1])), c2, nm2);
-            const float2 pe = ex2_pair<kPromptPoly>(y, e);
+            const float2 pe = make_float2(ex2(y.x), ex2(y.y));
             sum[e & 3] = add2(sum[e & 3], pe);
             pk[e] = pack_bf16x2(pe.x, pe.y);
           }
@@ -517,10 +481,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int64_t tok = int64_t(w.s.q0) + q, hq = int64_t(h) * p.g + r % p.g;
         const bool any = lim > 0 && nk[t] > 0;
         if (row_ok) {
-          if (any && !(l > 0.f && l < kNoSum)) {
-            status_or(a.status, RMM_NONFINITE_BIT);
-            l = NAN;
-          }
+          if (any && !(l > 0.f && l < INFINITY)) status_or(a.status, RMM_NONFINITE_BIT);
           if (a.lse) a.lse[hq * a.T_q + tok] = any ? (log2f(l) - nm) * kLn2 : -INFINITY;
         }
         const float inv = any ? 1.0f / l : 0.f;
@@ -848,7 +809,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                     if (col + 1 < lo || col + 1 >= hi) y[z].y = -INFINITY;
                   }
                   float2& sum = part[((e >> 1) + z) & 3];
-                  sum = add2(sum, ex2_pair<kWeightsPoly>(y[z], (e >> 1) + z));
+                  sum = add2(sum, make_float2(ex2(y[z].x), ex2(y[z].y)));
                 }
               }
             };
@@ -891,10 +852,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
       } else {
         for (uint32_t r = 0; r < p.split; ++r) x += ld_cluster_f32(mapa_shared(smem_addr(sum_sh + i), r));
       }
-      if (!(x < kNoSum)) {
-        status_or(a.status, RMM_NONFINITE_BIT);
-        x = NAN;
-      }
+      if (!isfinite(x)) status_or(a.status, RMM_NONFINITE_BIT);
       const int64_t at = int64_t(h) * a.T_k + w.s.k0 + k;
       a.w_out[at] = a.w_in ? a.w_in[at] + x : x;
     }
