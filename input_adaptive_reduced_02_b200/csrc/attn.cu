@@ -185,8 +185,9 @@ struct PromptCfg {
   static constexpr int BOXES = DP / 64;
   static constexpr uint32_t BOX = kRows * 128;       // 128 rows x 64 bf16
   static constexpr uint32_t TILE = BOXES * BOX;      // one Q, K or V tile
-  static constexpr int STAGES = DP == 128 ? 5 : 8;   // K and V tiles in flight
-  static constexpr size_t SMEM = 1024 + size_t(2 + STAGES) * TILE + 256;
+  static constexpr int STAGES = DP == 128 ? 4 : 8;   // K and V tiles in flight
+  static constexpr uint32_t STAGING = 8 * 32 * 128;  // 128 bytes of each output row
+  static constexpr size_t SMEM = 1024 + size_t(2 + STAGES) * TILE + STAGING + 256;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -200,7 +201,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(attn_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                   // two tiles
   uint8_t* sKV = sQ + 2 * Cfg::TILE;    // ring
-  uint64_t* full = reinterpret_cast<uint64_t*>(sKV + STAGES * Cfg::TILE);
+  uint8_t* staging = sKV + STAGES * Cfg::TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING);
   uint64_t* empty = full + STAGES;
   uint64_t* q_full = empty + STAGES;    // [2]
   uint64_t* s_full = q_full + 2;        // [2] S_t ready (and O_t up to the previous key tile)
@@ -485,31 +487,49 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (a.lse) a.lse[hq * a.T_q + tok] = any ? (log2f(l) - nm) * kLn2 : -INFINITY;
         }
         const float inv = any ? 1.0f / l : 0.f;
+        // Rows leave through shared memory, so that a store instruction covers whole
+        // 128-byte pieces of four of them (a thread's own row lies 16 bytes to each).
+        uint8_t* mine = staging + warp * (32 * 128);
+        const int64_t row_at = row_ok ? tok * a.o_ts + hq * a.o_hs : -1;
+        auto leave = [&](int col0, int per) {  // per: channels of 16 bytes
+          __syncwarp();
+          const int col = col0 + (lane & 7) * per;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            const int64_t at = __shfl_sync(0xffffffffu, row_at, row) + col;
+            const uint4 v = *reinterpret_cast<const uint4*>(mine + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+            if (at < col || col >= a.d) continue;
+            if (a.out == kBF16)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at) = v;
+            else
+              *reinterpret_cast<uint4*>(static_cast<float*>(a.o) + at) = v;
+          }
+          __syncwarp();
+        };
 #pragma unroll
         for (int x = 0; x < DP / 32; ++x) {
           uint32_t o[32];
-          __syncwarp();
           if (nk[t] > 0) {
             tmem_ld_32x32b_x32(tO + 32 * x, o);
-            tmem_ld_wait();
+            tmem_ld_wait(o);
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-          if (!row_ok) continue;
+          if (a.out == kBF16) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int col = 32 * x + 8 * v;
-            if (col >= a.d) break;
-            const uint32_t* e = o + 8 * v;
-            const int64_t at = tok * a.o_ts + hq * a.o_hs + col;
-            if (a.out == kBF16) {
-              auto two = [&](int i) { return pack_bf16x2(__uint_as_float(e[i]), __uint_as_float(e[i + 1])); };
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at) = make_uint4(two(0), two(2), two(4), two(6));
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(a.o) + at);
-              dst[0] = make_uint4(e[0], e[1], e[2], e[3]);
-              dst[1] = make_uint4(e[4], e[5], e[6], e[7]);
+            for (int v = 0; v < 4; ++v) {
+              auto two = [&](int i) { return pack_bf16x2(__uint_as_float(o[8 * v + i]), __uint_as_float(o[8 * v + i + 1])); };
+              *reinterpret_cast<uint4*>(mine + lane * 128 + (((4 * (x & 1) + v) ^ (lane & 7)) << 4)) =
+                  make_uint4(two(0), two(2), two(4), two(6));
             }
+            if (x & 1) leave(32 * (x - 1), 8);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              *reinterpret_cast<uint4*>(mine + lane * 128 + ((v ^ (lane & 7)) << 4)) =
+                  make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            leave(32 * x, 4);
           }
         }
       }

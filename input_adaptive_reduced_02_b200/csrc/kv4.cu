@@ -35,13 +35,6 @@ __device__ __forceinline__ int64_t find_seq(const int32_t* cu, int64_t n, int64_
 // Bound by HBM for whole prompts: 2·d values read, 2·(d/2 + d/8) bytes written.
 constexpr int kStoreThreads = 256;
 
-// rint(x / s) for x / s in about [-1, 17]: the product with the reciprocal is
-// within 2^-17 of the quotient, so only next to a half does it take the division.
-__device__ __forceinline__ float rounded_quotient(float x, float s, float inv) {
-  const float q = x * inv, r = rintf(q);
-  return fabsf(fabsf(q - r) - 0.5f) > 0x1p-15f ? r : rintf(__fdiv_rn(x, s));
-}
-
 template <typename T>
 __device__ __forceinline__ void load8(float (&f)[8], const T* p, bool vec) {
   if (vec) {
@@ -66,6 +59,34 @@ __device__ __forceinline__ void load8(float (&f)[8], const T* p, bool vec) {
   }
 }
 
+// The 8 codes of x, nibble e for x[e]: rint((x - mn) / step) within 0 .. 15.
+// The product with the reciprocal is within 2^-17 of the quotient (about -1 to
+// 17), so only where one lands next to a half, or where the reciprocal is no
+// normal number, are the divisions made.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float step, float mn) {
+  if (!(step > 0.f)) return 0;
+  const float inv = 1.0f / step;
+  float r[8], far = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // the nearest integer, by an addition that leaves no bits below 1 (exact for quotients below 2^22)
+    const float q = (x[e] - mn) * inv;
+    r[e] = __fsub_rn(__fadd_rn(q, 12582912.f), 12582912.f);
+    far = fmaxf(far, fabsf(q - r[e]));
+  }
+  if (!(far < 0.5f - 0x1p-15f && step > 0x1p-120f && step < 0x1p120f)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = rintf(__fdiv_rn(x[e] - mn, step));
+  }
+  float acc[2] = {0.f, 0.f};  // four codes each as one number below 2^16
+#pragma unroll
+  for (int e = 3; e >= 0; --e) {
+    acc[0] = fmaf(acc[0], 16.f, fminf(fmaxf(r[e], 0.f), 15.f));
+    acc[1] = fmaf(acc[1], 16.f, fminf(fmaxf(r[4 + e], 0.f), 15.f));
+  }
+  return uint32_t(acc[0]) | uint32_t(acc[1]) << 16;
+}
+
 template <typename T, int NG>
 __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4StoreArgs a, bool vec) {
   constexpr int LANES = 4 * NG, ROWS = kStoreThreads / LANES;
@@ -73,33 +94,33 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
   pdl_wait();
   const int row = threadIdx.x / LANES, u = threadIdx.x % LANES;
   const int64_t h = blockIdx.y;
+  const int w = u >> 2, j = u & 3;  // group, quarter of the group
   const int64_t t = int64_t(blockIdx.x) * ROWS + row;
   bool live = row < ROWS && t < a.T;
   const int64_t tc = min(t, a.T - 1);  // surplus threads repeat the last token and store nothing
-  float f[2][8];
-  load8(f[0], static_cast<const T*>(a.k.ptr) + tc * a.k.ts + h * a.k.hs + 8 * u, vec);
-  load8(f[1], static_cast<const T*>(a.v.ptr) + tc * a.v.ts + h * a.v.hs + 8 * u, vec);
-  int64_t b = tc, in_seq = 0;
+  float x[2][8];
+  load8(x[0], static_cast<const T*>(a.k.ptr) + tc * a.k.ts + h * a.k.hs + 8 * u, vec);
+  load8(x[1], static_cast<const T*>(a.v.ptr) + tc * a.v.ts + h * a.v.hs + 8 * u, vec);
+  int64_t b = tc, first = tc;
   if (a.cu) {
     b = find_seq(a.cu, a.n_seq, tc);
-    in_seq = tc - a.cu[b];
-    live = live && in_seq >= 0 && tc < a.cu[b + 1];
+    first = a.cu[b];
+    live = live && tc >= first && tc < a.cu[b + 1];
   }
-  const int64_t slot = int64_t(a.start[b]) + in_seq;
+  const int64_t slot = int64_t(a.start[b]) + (tc - first);
   const bool in_cache = slot >= 0 && slot < a.cap;
-  const int w = u >> 2, j = u & 3;  // group, quarter of the group
   const int64_t at = (b * a.h_kv + h) * a.cap + slot;
-  bool bad = false;
+  bool odd = false;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    const float* x = f[kv];
-    float lo = x[0], hi = x[0];
+    float lo = x[kv][0], hi = lo, zero = 0.f;  // zero: NaN where an element is NaN or infinite
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
-      bad |= !isfinite(x[e]);
+      lo = fminf(lo, x[kv][e]);
+      hi = fmaxf(hi, x[kv][e]);
+      zero = fmaf(x[kv][e], 0.f, zero);
     }
+    odd |= zero != 0.f;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -107,25 +128,15 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
     }
     // (step, minimum) as stored; the IEEE quotient, so that it depends on nothing but the values
     const uint32_t sm = pack_bf16x2(__fdiv_rn(hi - lo, 15.0f), lo);
-    const float step = __uint_as_float(sm << 16), mn = __uint_as_float(sm & 0xFFFF0000u);
-    const float inv = 1.0f / step;
-    // a step whose reciprocal is no normal number takes the division throughout
-    const bool near = step > 0x1p-120f && step < 0x1p120f;
-    uint32_t codes = 0;  // nibble e: channel 8u + e
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float q = 0.f;
-      if (step > 0.f) q = near ? rounded_quotient(x[e] - mn, step, inv) : rintf(__fdiv_rn(x[e] - mn, step));
-      codes |= uint32_t(fminf(fmaxf(q, 0.f), 15.f)) << (4 * e);
-    }
+    const uint32_t codes = codes_of(x[kv], __uint_as_float(sm << 16), __uint_as_float(sm & 0xFFFF0000u));
     // the values' half-words need one nibble from each of the group's four lanes
     uint32_t half[2] = {0u, 0u};  // half-words r = 2j, 2j + 1 of group w
     if (kv == 1) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const uint32_t c = __shfl_sync(0xffffffffu, codes, (threadIdx.x & 28) | s);
-        half[0] |= ((c >> (8 * j)) & 15u) << (4 * s);
-        half[1] |= ((c >> (8 * j + 4)) & 15u) << (4 * s);
+        const uint32_t c = __shfl_sync(0xffffffffu, codes, (threadIdx.x & 28) | s) >> (8 * j);
+        half[0] |= (c & 15u) << (4 * s);
+        half[1] |= ((c >> 4) & 15u) << (4 * s);
       }
     }
     if (!live || !in_cache) continue;
@@ -139,14 +150,12 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
     }
   }
   if (!live) return;
-  if (bad) status_or(a.status, RMM_NONFINITE_BIT);
-  if (!in_cache) {
+  if (odd) status_or(a.status, RMM_NONFINITE_BIT);
+  if (!in_cache)
     status_or(a.status, RMM_RANGE_BIT);
-  } else if (u == 0 && a.w) {
+  else if (u == 0 && a.w)
     a.w[at] = a.w_new ? a.w_new[h * a.T + t] : 0.f;
-  }
 }
-
 // ---------------------------------------------------------------- attention
 // The work is the tiles of 16 tokens of every item (sequence, key head, chunk
 // of its query heads) with tokens, one item after the other; CTA c takes tiles
