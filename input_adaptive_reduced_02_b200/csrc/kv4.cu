@@ -8,6 +8,7 @@
 // m, a bf16 step s = bf16((max - min) / 15) and per channel a 4-bit code
 // c = clamp(rint((x - m) / s), 0, 15), 0 where s is 0; it stands for m + s·c.
 #include <algorithm>
+#include <type_traits>
 
 #include "rmm_device.cuh"
 #include "rmm_internal.h"
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
     a.w[at] = a.w_new ? a.w_new[h * a.T + t] : 0.f;
 }
 // ---------------------------------------------------------------- attention
-// The work is the tiles of 16 tokens of every item (sequence, key head, chunk
+// The work is the tiles of 16 or 32 tokens of every item (sequence, key head, chunk
 // of its query heads) with tokens, one item after the other; CTA c takes tiles
 // [c·per, (c+1)·per) of the line, whichever items they are of, so ragged
 // lengths leave no SM idle. A part of an item that one CTA works on is one
@@ -170,6 +171,7 @@ struct Kv4Dev {
   float* scores;  // [batch][h_kv][cap][h_q / h_kv] log2 units, or null
   int64_t* line;  // [batch + 1] first tile of each sequence, then all tiles; [batch + 1] tiles per CTA
   int32_t chunks, chunk_heads;  // per key head; query heads of a chunk
+  int32_t tile;                 // tokens of a tile
 };
 
 __device__ __forceinline__ int32_t seq_len(const Kv4AttnArgs& a, int64_t b) {
@@ -195,17 +197,23 @@ __device__ __forceinline__ int32_t seq_len(const Kv4AttnArgs& a, int64_t b) {
 //       from 2^-57 (smaller ones fade out) up to 2^62.
 // So a word of 8 codes costs one shift and four masks. What bounds the kernel
 // is the rate of such instructions, then HBM.
-// A tile's bytes come by cp.async through a ring per warp, kKvStages - 1 tiles
+// With up to 4 query heads per key head a tile has two halves of 16 tokens: the
+// second half's scores and outputs take columns 4-7 of the same accumulators (B
+// is zero in the other half's columns), so that no lane's scaling, exponentials
+// and scales are spent on columns without a head (batch of 32 x 8192, 4 heads:
+// 91 us without, 86 with).
+// A tile's bytes come by cp.async through a ring per warp, STAGES - 1 tiles
 // ahead; rows past the length arrive as zeros.
 constexpr int kKvWarps = 8;
-constexpr int kKvStages = 4;
 constexpr float kKvRescale = 8.0f;  // log2 of the growth of p that is let through unscaled
 
-template <int NG>
+template <int NG, int HALVES>
 struct KvTile {
-  static constexpr int CODES = 16 * 16 * NG;  // bytes of 16 rows of codes
-  static constexpr int SCALES = 16 * 4 * NG;
+  static constexpr int TOKENS = 16 * HALVES;
+  static constexpr int CODES = TOKENS * 16 * NG;  // bytes of the rows of codes
+  static constexpr int SCALES = TOKENS * 4 * NG;
   static constexpr int BYTES = 2 * (CODES + SCALES);
+  static constexpr int STAGES = 4 / HALVES;
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
@@ -309,14 +317,17 @@ __device__ __forceinline__ int64_t div_up(int64_t x, int64_t y) {
   return (x + y - 1) / y;
 }
 
-template <int NG, int NT>
+template <int NG, int NT, int HALVES>
 __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split_kernel(const Kv4Dev p) {
-  using Tile = KvTile<NG>;
-  constexpr int D = 32 * NG, HEADS = 8 * NT;
+  using Tile = KvTile<NG, HALVES>;
+  constexpr int D = 32 * NG, HEADS = 8 * NT, STAGES = Tile::STAGES, TT = Tile::TOKENS;
+  constexpr int SETS = NT * HALVES;  // operands of Sᵀ: of 8 heads each, or of the heads in one half's columns
+  static_assert(NT == 1 || HALVES == 1, "halves share one tile of columns");
   extern __shared__ __align__(16) uint8_t kv_smem[];  // [warps][stages][tile], then the outputs
   __shared__ float m_sh[kKvWarps][HEADS], l_sh[kKvWarps][HEADS];
   __shared__ int64_t sums_sh[kKvWarps], b_sh, before_sh;
-  static_assert(kKvStages * Tile::BYTES >= HEADS * D * 4, "a warp's ring holds its outputs at the end");
+  __shared__ uint4 q_sh[SETS][SETS == 1 ? 1 : NG][SETS == 1 ? 1 : 32];  // the warps' common operand of Sᵀ
+  static_assert(STAGES * Tile::BYTES >= HEADS * D * 4, "a warp's ring holds its outputs at the end");
   pdl_trigger();
   pdl_wait();
   const Kv4AttnArgs& a = p.a;
@@ -332,7 +343,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     const int64_t each = (a.batch + kKvWarps * 32 - 1) / (kKvWarps * 32);
     const int64_t s0 = min(tid * each, a.batch), s1 = min(s0 + each, a.batch);
     int64_t mine = 0;
-    for (int64_t i = s0; i < s1; ++i) mine += int64_t((seq_len(a, i) + 15) / 16) * seq_items;
+    for (int64_t i = s0; i < s1; ++i) mine += int64_t((seq_len(a, i) + TT - 1) / TT) * seq_items;
     const LinePos at = line_scan(mine, sums_sh, tid);
     // at least as many tiles as an item has on average, up to one per warp: fewer partial results to join
     const int64_t per = max(max(div_up(at.all, gridDim.x), int64_t(1)),
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     end = min(pos + per, at.all);
     int64_t before = at.before;
     for (int64_t i = s0; i < s1; ++i) {
-      const int64_t n = int64_t((seq_len(a, i) + 15) / 16) * seq_items;
+      const int64_t n = int64_t((seq_len(a, i) + TT - 1) / TT) * seq_items;
       if (before <= pos && pos < before + n) {
         b_sh = i;
         before_sh = before;
@@ -357,10 +368,10 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   if (pos >= end) return;
   __syncthreads();
   int64_t b = b_sh;
-  int32_t len = seq_len(a, b), item_tiles = (len + 15) / 16;
+  int32_t len = seq_len(a, b), item_tiles = (len + TT - 1) / TT;
   int32_t in_seq = int32_t(div_up(pos - before_sh + 1, item_tiles)) - 1;  // item of the sequence: (key head, chunk)
   int32_t first = int32_t(pos - before_sh - int64_t(in_seq) * item_tiles);
-  uint8_t* ring = kv_smem + warp * (kKvStages * Tile::BYTES);
+  uint8_t* ring = kv_smem + warp * (STAGES * Tile::BYTES);
 
   for (;;) {  // a part: tiles [first, first + tiles) of an item
   const int32_t tiles = int32_t(min(int64_t(item_tiles - first), end - pos));
@@ -368,76 +379,65 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   const int32_t head0 = int32_t(in_seq % p.chunks) * HEADS;  // first of the chunk's heads within the group
   const int64_t hq0 = (item - b * a.h_kv) * gq + head0;
   const int32_t heads = min(HEADS, gq - head0);
-  const int32_t t0 = 16 * first, t1 = min(len, t0 + 16 * tiles);
+  const int32_t t0 = TT * first, t1 = min(len, t0 + TT * tiles);
   const int64_t slot = blockIdx.x + b * seq_items + in_seq;
 
-  // a lane's 16-byte pieces of a tile's codes (keys', then values') and pieces of its scales
   const int64_t row0 = item * a.cap + t0;
-  constexpr int SP = NG == 4 ? 1 : NG;            // pieces of scales per lane: rows of 16 bytes are copied whole
-  constexpr int SB = NG == 4 ? 16 : 4;            // their bytes
-  const uint8_t *code_src[NG], *scale_src[SP];
-#pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    const int c = lane + 32 * i;
-    code_src[i] = (c < 16 * NG ? a.c.kc + 16 * c : a.c.vc + 16 * (c - 16 * NG)) + row0 * (16 * NG);
-  }
-#pragma unroll
-  for (int i = 0; i < SP; ++i) {
-    const int c = (lane + 32 * i) * SB;
-    scale_src[i] = reinterpret_cast<const uint8_t*>(c < Tile::SCALES ? a.c.ks : a.c.vs) +
-                   (c < Tile::SCALES ? c : c - Tile::SCALES) + row0 * (4 * NG);
-  }
   const int32_t rows = t1 - t0;
-  auto load = [&](int32_t tile, uint8_t* dst) {
-    const int64_t off = int64_t(tile) * Tile::CODES, soff = int64_t(tile) * Tile::SCALES;
-    const int32_t live = rows - 16 * tile;
-    uint8_t* to = dst + 16 * lane;
-    uint8_t* sto = dst + 2 * Tile::CODES + SB * lane;
-    if (live >= 16) {
+  constexpr int SB = NG == 4 ? 16 : 4;  // bytes of a piece of the scales: rows of 16 bytes are copied whole
+  // one plane's rows of a tile, in pieces of SIZE bytes; rows past the length become zeros
+  auto copy = [&](auto size, auto total, uint8_t* dst, const uint8_t* src, int32_t live_bytes) {
+    constexpr int SIZE = decltype(size)::value, PIECES = decltype(total)::value / SIZE;
 #pragma unroll
-      for (int i = 0; i < NG; ++i) cp_async16(to + 512 * i, code_src[i] + off, 16);
-#pragma unroll
-      for (int i = 0; i < SP; ++i) {
-        if constexpr (SB == 16)
-          cp_async16(sto, scale_src[i] + soff, 16);
-        else
-          cp_async4(sto + 32 * SB * i, scale_src[i] + soff, 4);
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {  // rows past the length: zeros, and an address within the cache
-      const int c = (lane + 32 * i) * 16, in_plane = c < Tile::CODES ? c : c - Tile::CODES;
-      const bool in = in_plane < live * 16 * NG;
-      cp_async16(to + 512 * i, in ? code_src[i] + off : code_src[i] + off - in_plane, in ? 16 : 0);
-    }
-#pragma unroll
-    for (int i = 0; i < SP; ++i) {
-      const int c = (lane + 32 * i) * SB, in_plane = c < Tile::SCALES ? c : c - Tile::SCALES;
-      const bool in = in_plane < live * 4 * NG;
-      const uint8_t* src = scale_src[i] + soff - (in ? 0 : in_plane);
-      if constexpr (SB == 16)
-        cp_async16(sto, src, in ? 16 : 0);
+    for (int i = 0; i < (PIECES + 31) / 32; ++i) {
+      const int off = (lane + 32 * i) * SIZE;
+      if (PIECES % 32 != 0 && lane + 32 * i >= PIECES) continue;
+      const bool in = off < live_bytes;
+      if constexpr (SIZE == 16)
+        cp_async16(dst + off, in ? src + off : src, in ? 16 : 0);
       else
-        cp_async4(sto + 32 * SB * i, src, in ? 4 : 0);
+        cp_async4(dst + off, in ? src + off : src, in ? 4 : 0);
     }
   };
+  const uint8_t *k_src = a.c.kc + row0 * (16 * NG), *v_src = a.c.vc + row0 * (16 * NG);
+  const uint8_t* ks_src = reinterpret_cast<const uint8_t*>(a.c.ks) + row0 * (4 * NG);
+  const uint8_t* vs_src = reinterpret_cast<const uint8_t*>(a.c.vs) + row0 * (4 * NG);
+  auto load = [&](int32_t tile, uint8_t* dst) {
+    using Codes = std::integral_constant<int, Tile::CODES>;
+    using Scales = std::integral_constant<int, Tile::SCALES>;
+    const int64_t off = int64_t(tile) * Tile::CODES, soff = int64_t(tile) * Tile::SCALES;
+    const int32_t live = rows - TT * tile;
+    auto all = [&](int32_t code_bytes, int32_t scale_bytes) {
+      copy(std::integral_constant<int, 16>(), Codes(), dst, k_src + off, code_bytes);
+      copy(std::integral_constant<int, 16>(), Codes(), dst + Tile::CODES, v_src + off, code_bytes);
+      copy(std::integral_constant<int, SB>(), Scales(), dst + 2 * Tile::CODES, ks_src + soff, scale_bytes);
+      copy(std::integral_constant<int, SB>(), Scales(), dst + 2 * Tile::CODES + Tile::SCALES, vs_src + soff, scale_bytes);
+    };
+    if (live >= TT)
+      all(Tile::CODES, Tile::SCALES);
+    else
+      all(live * (16 * NG), live * (4 * NG));
+  };
 #pragma unroll
-  for (int s = 0; s < kKvStages - 1; ++s) {
+  for (int s = 0; s < STAGES - 1; ++s) {
     const int32_t tile = warp + s * kKvWarps;
     if (tile < tiles) load(tile, ring + s * Tile::BYTES);
     cp_async_commit();
   }
 
-  // Queries of head r (of each n tile), channels 32g + 8j .. + 7: the operand of Sᵀ.
-  // Then of heads 2j, 2j+1, what their scores are made of.
-  uint32_t qb[NT][NG][4];
-  uint32_t qsum[NT][2];  // head r's sum of q over group j as three bf16 parts
+  // Queries of the head of column r (of each n tile), channels 32g + 8j .. + 7:
+  // the operand of Sᵀ. Then of columns 2j, 2j+1, what their scores are made of.
+  const int lh = HALVES == 2 ? j >> 1 : 0;  // half of the tile that columns 2j, 2j+1 are of
+  auto head_of = [](int col) { return HALVES == 2 ? col & 3 : col; };
+  // One operand stays in registers; two are read again from shared memory.
+  uint32_t qsum[SETS][2];  // head r's sum of q over group j as three bf16 parts
+  uint4 q_reg[SETS == 1 ? NG : 1];
   float fh[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const bool live = 8 * n + r < heads;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_ss + (hq0 + (live ? 8 * n + r : 0)) * a.q_hs;
+    const int head = 8 * n + head_of(r);
+    const bool live = head < heads;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_ss + (hq0 + (live ? head : 0)) * a.q_hs;
     uint32_t w[NG][4];
     uint32_t top = 0;  // largest magnitude, as its bf16 bits
     float sum[NG];
@@ -473,7 +473,18 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float k = c % 2 ? 0.0625f : 1.0f;
-        qb[n][g][c] = pack_f16x2(f[c] * k, f[c + 4] * k);
+        f[c] = __uint_as_float(pack_f16x2(f[c] * k, f[c + 4] * k));
+      }
+      {
+        const uint4 u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                   __float_as_uint(f[3]));
+        if constexpr (SETS == 1) {
+          q_reg[g] = u;
+        } else if (warp == 0) {
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            q_sh[n + h][g][lane] = HALVES == 1 || r >> 2 == h ? u : make_uint4(0u, 0u, 0u, 0u);
+        }
       }
     }
     float qs = sum[0];
@@ -483,11 +494,17 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     qs = j < NG ? qs * mul * 0x1p-24f : 0.f;
     const uint32_t hi = pack_bf16x2(qs, 0.f) << 16;
     const float rest = qs - __uint_as_float(hi);
-    qsum[n][0] = pack_bf16x2(qs, rest);
-    qsum[n][1] = pack_bf16x2(rest - __uint_as_float(qsum[n][0] & 0xFFFF0000u), 0.f);
+    const uint32_t parts = pack_bf16x2(qs, rest);
+    const uint32_t last = pack_bf16x2(rest - __uint_as_float(parts & 0xFFFF0000u), 0.f);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      const bool mine = HALVES == 1 || r >> 2 == h;
+      qsum[n + h][0] = mine ? parts : 0u;
+      qsum[n + h][1] = mine ? last : 0u;
+    }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int32_t eh = __shfl_sync(0xffffffffu, e, 4 * (2 * j + x));  // a lane that holds head 2j + x
+      const int32_t eh = __shfl_sync(0xffffffffu, e, 4 * (2 * j + x));  // a lane that holds column 2j + x
       fh[n][x] = a.scale * 1.4426950408889634f * 0x1p24f * __uint_as_float(uint32_t(127 + eh) << 23);
     }
   }
@@ -508,48 +525,56 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     }
   }
 
+  if constexpr (SETS > 1) __syncthreads();  // q_sh is written
   int stage = 0;
   for (int32_t tile = warp; tile < tiles; tile += kKvWarps) {
     {
-      const int32_t ahead = tile + (kKvStages - 1) * kKvWarps;
-      const int s = stage == 0 ? kKvStages - 1 : stage - 1;
+      const int32_t ahead = tile + (STAGES - 1) * kKvWarps;
+      const int s = stage == 0 ? STAGES - 1 : stage - 1;
       if (ahead < tiles) load(ahead, ring + s * Tile::BYTES);
       cp_async_commit();
     }
-    cp_async_wait<kKvStages - 1>();
+    cp_async_wait<STAGES - 1>();
     __syncwarp();
     const uint8_t* buf = ring + stage * Tile::BYTES;
     const uint8_t *kc = buf, *vc = buf + Tile::CODES, *ks = buf + 2 * Tile::CODES, *vs = ks + Tile::SCALES;
-    const int32_t tok = t0 + 16 * tile + r;  // tokens tok and tok + 8
+    const int32_t tok = t0 + TT * tile + 16 * lh + r;  // tokens tok and tok + 8
 
     // ---- scores
     float t[NT][4];
     {
-      uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
-      lds_words<NG>(w0, kc + r * (16 * NG) + j * (4 * NG));
-      lds_words<NG>(w1, kc + (r + 8) * (16 * NG) + j * (4 * NG));
-      lds_words<NG>(s0, ks + r * (4 * NG));
-      lds_words<NG>(s1, ks + (r + 8) * (4 * NG));
+      uint32_t w0[HALVES][NG], w1[HALVES][NG], s0[NG], s1[NG];
+      lds_words<NG>(s0, ks + (16 * lh + r) * (4 * NG));
+      lds_words<NG>(s1, ks + (16 * lh + r + 8) * (4 * NG));
       const int jg = NG == 4 ? j : min(j, NG - 1);
-      const uint32_t m0 = __byte_perm(*reinterpret_cast<const uint32_t*>(ks + r * (4 * NG) + 4 * jg), 0, 0x3232);
-      const uint32_t m1 = __byte_perm(*reinterpret_cast<const uint32_t*>(ks + (r + 8) * (4 * NG) + 4 * jg), 0, 0x3232);
-      const uint32_t mins[4] = {m0, m1, m0, m1};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
-        mma_bf16(t[n], mins, qsum[n][0], qsum[n][1]);
+      for (int n = 0; n < NT; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const uint8_t *k0 = kc + (16 * h + r) * (16 * NG) + j * (4 * NG), *m = ks + (16 * h + r) * (4 * NG) + 4 * jg;
+        lds_words<NG>(w0[h], k0);
+        lds_words<NG>(w1[h], k0 + 8 * (16 * NG));
+        const uint32_t m0 = __byte_perm(*reinterpret_cast<const uint32_t*>(m), 0, 0x3232);
+        const uint32_t m1 = __byte_perm(*reinterpret_cast<const uint32_t*>(m + 8 * (4 * NG)), 0, 0x3232);
+        const uint32_t mins[4] = {m0, m1, m0, m1};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_bf16(t[n], mins, qsum[n + h][0], qsum[n + h][1]);
       }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const uint32_t h0 = w0[g] >> 8, h1 = w1[g] >> 8;
-        const uint32_t lo[4] = {w0[g] & 0x000F000Fu, w1[g] & 0x000F000Fu, w0[g] & 0x00F000F0u, w1[g] & 0x00F000F0u};
-        const uint32_t hi[4] = {h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x00F000F0u};
         const float st0 = step_of(s0[g]), st1 = step_of(s1[g]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(c, lo, qb[n][g][0], qb[n][g][1]);
-          mma_f16(c, hi, qb[n][g][2], qb[n][g][3]);
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            const uint32_t x0 = w0[h][g], x1 = w1[h][g], h0 = x0 >> 8, h1 = x1 >> 8;
+            const uint32_t lo[4] = {x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u};
+            const uint32_t hi[4] = {h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x00F000F0u};
+            const uint4 q = SETS == 1 ? q_reg[SETS == 1 ? g : 0] : q_sh[n + h][g][lane];
+            mma_f16(c, lo, q.x, q.y);
+            mma_f16(c, hi, q.z, q.w);
+          }
           t[n][0] = fmaf(c[0], st0, t[n][0]);
           t[n][1] = fmaf(c[1], st0, t[n][1]);
           t[n][2] = fmaf(c[2], st1, t[n][2]);
@@ -563,11 +588,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (8 * n + 2 * j + x < heads) {
-            if (in0) dst[8 * n + 2 * j + x] = t[n][x] * fh[n][x];
-            if (in1) dst[8 * gq + 8 * n + 2 * j + x] = t[n][2 + x] * fh[n][x];
-          }
+        for (int x = 0; x < 2; ++x) {
+          const int head = 8 * n + head_of(2 * j + x);
+          if (head >= heads) continue;
+          if (in0) dst[head] = t[n][x] * fh[n][x];
+          if (in1) dst[8 * gq + head] = t[n][2 + x] * fh[n][x];
+        }
     }
     // ---- softmax: p = 2^(t·fh - maximum), the maximum one the whole warp uses
     float pr[NT][4];
@@ -579,7 +605,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
         pr[n][c] = fmaf(t[n][c], fh[n][c & 1], nm[n][c & 1]);
         top = fmaxf(top, pr[n][c]);
       }
-    const bool tail = 16 * tile + 16 > rows;
+    const bool tail = TT * tile + TT > rows;
     if (__any_sync(0xffffffffu, tail || top > kKvRescale)) {
       if (tail) {
 #pragma unroll
@@ -592,12 +618,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          // fh is positive; -inf stays out of the maximum, which some token of every tile reaches
+          // fh is positive. A column of the second half may have no token yet: its maximum stays -inf.
           float mx = fmaxf(t[n][x], t[n][2 + x]) * fh[n][x];
 #pragma unroll
           for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
           const float nm2 = fminf(nm[n][x], -mx);
-          const float f = ex2f(nm2 - nm[n][x]);  // 0 the first time
+          const float f = nm2 == nm[n][x] ? 1.f : ex2f(nm2 - nm[n][x]);  // 0 the first time
           nm[n][x] = nm2;
           l[n][x] *= f;
 #pragma unroll
@@ -609,8 +635,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
               o[n][2 * g + u][2 + x] *= f;
             }
           }
-          pr[n][x] = fmaf(t[n][x], fh[n][x], nm2);
-          pr[n][2 + x] = fmaf(t[n][2 + x], fh[n][x], nm2);
+          pr[n][x] = t[n][x] == -INFINITY ? -INFINITY : fmaf(t[n][x], fh[n][x], nm2);
+          pr[n][2 + x] = t[n][2 + x] == -INFINITY ? -INFINITY : fmaf(t[n][2 + x], fh[n][x], nm2);
         }
     }
 #pragma unroll
@@ -626,28 +652,40 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 4; ++c) big[n][c] = pr[n][c] * 0x1p64f;
-    uint32_t wl[NG], wh[NG], s0[NG], s1[NG];
-    pair_halves<NG>(wl, vc + (2 * j) * (16 * NG) + r * (2 * NG), vc + (2 * j + 1) * (16 * NG) + r * (2 * NG));
-    pair_halves<NG>(wh, vc + (2 * j + 8) * (16 * NG) + r * (2 * NG), vc + (2 * j + 9) * (16 * NG) + r * (2 * NG));
-    lds_words<NG>(s0, vs + r * (4 * NG));
-    lds_words<NG>(s1, vs + (r + 8) * (4 * NG));
+    uint32_t wl[HALVES][NG], wh[HALVES][NG], s0[NG], s1[NG];
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      const uint8_t* v0 = vc + (16 * h + 2 * j) * (16 * NG) + r * (2 * NG);
+      pair_halves<NG>(wl[h], v0, v0 + 16 * NG);
+      pair_halves<NG>(wh[h], v0 + 8 * (16 * NG), v0 + 9 * (16 * NG));
+    }
+    lds_words<NG>(s0, vs + (16 * lh + r) * (4 * NG));
+    lds_words<NG>(s1, vs + (16 * lh + r + 8) * (4 * NG));
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const float st0 = step_of(s0[g]), mn0 = min_of(s0[g]), st1 = step_of(s1[g]), mn1 = min_of(s1[g]);
-      const uint32_t hl = wl[g] >> 8, hh = wh[g] >> 8;
-      const uint32_t av[2][4] = {{wl[g] & 0x000F000Fu, wl[g] & 0x00F000F0u, wh[g] & 0x000F000Fu, wh[g] & 0x00F000F0u},
-                                 {hl & 0x000F000Fu, hl & 0x00F000F0u, hh & 0x000F000Fu, hh & 0x00F000F0u}};
+      uint32_t b0[NT], b1[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint32_t b0 = movmatrix_trans(pack_bf16x2(big[n][0] * st0, big[n][1] * st0));
-        const uint32_t b1 = movmatrix_trans(pack_bf16x2(big[n][2] * st1, big[n][3] * st1));
+        b0[n] = movmatrix_trans(pack_bf16x2(big[n][0] * st0, big[n][1] * st0));
+        b1[n] = movmatrix_trans(pack_bf16x2(big[n][2] * st1, big[n][3] * st1));
         om[n][g][0] = fmaf(pr[n][0], mn0, fmaf(pr[n][2], mn1, om[n][g][0]));
         om[n][g][1] = fmaf(pr[n][1], mn0, fmaf(pr[n][3], mn1, om[n][g][1]));
-        mma_bf16(o[n][2 * g], av[0], b0, b1);
-        mma_bf16(o[n][2 * g + 1], av[1], b0, b1);
+      }
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const uint32_t x0 = wl[h][g], x1 = wh[h][g], h0 = x0 >> 8, h1 = x1 >> 8;
+        const uint32_t av[2][4] = {{x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u},
+                                   {h0 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x000F000Fu, h1 & 0x00F000F0u}};
+        const uint32_t cols = HALVES == 1 || r >> 2 == h ? 0xFFFFFFFFu : 0u;  // column r's half
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_bf16(o[n][2 * g], av[0], b0[n] & cols, b1[n] & cols);
+          mma_bf16(o[n][2 * g + 1], av[1], b0[n] & cols, b1[n] & cols);
+        }
       }
     }
-    stage = stage + 1 == kKvStages ? 0 : stage + 1;
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
     __syncwarp();  // the stage is free for the next load
   }
   cp_async_wait<0>();
@@ -681,29 +719,36 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
           mine[(8 * n + 2 * j + (c & 1)) * D + 32 * g + 16 * u + 8 * (c >> 1) + r] =
               fmaf(o[n][2 * g + u][c], c < 2 ? 0x1p69f : 0x1p65f, om[n][g][c & 1]);
   __syncthreads();
-  if (tid < heads) {  // m_sh becomes the warps' factors
+  if (tid < heads) {  // m_sh becomes the warps' factors (a head's second column: of the second half)
     float m = m_sh[0][tid];  // the first warp has a tile
 #pragma unroll
-    for (int w = 1; w < kKvWarps; ++w) m = fmaxf(m, m_sh[w][tid]);
+    for (int w = 0; w < kKvWarps; ++w)
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) m = fmaxf(m, m_sh[w][tid + 4 * h]);
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kKvWarps; ++w) {
-      const float f = ex2f(m_sh[w][tid] - m);
-      sum += l_sh[w][tid] * f;
-      m_sh[w][tid] = f;
-    }
+    for (int w = 0; w < kKvWarps; ++w)
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const float f = ex2f(m_sh[w][tid + 4 * h] - m);
+        sum += l_sh[w][tid + 4 * h] * f;
+        m_sh[w][tid + 4 * h] = f;
+      }
     *reinterpret_cast<float2*>(p.ml + 2 * (slot * HEADS + tid)) = make_float2(m, sum);
   }
   __syncthreads();
   for (int i = 4 * tid; i < heads * D; i += 4 * kKvWarps * 32) {
     float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kKvWarps; ++w) {
-      const float f = m_sh[w][i / D];
-      const float4 x = *reinterpret_cast<const float4*>(kv_smem + w * (kKvStages * Tile::BYTES) + 4 * i);
-      out.x = fmaf(x.x, f, out.x), out.y = fmaf(x.y, f, out.y);
-      out.z = fmaf(x.z, f, out.z), out.w = fmaf(x.w, f, out.w);
-    }
+    for (int w = 0; w < kKvWarps; ++w)
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const float f = m_sh[w][i / D + 4 * h];
+        const float4 x =
+            *reinterpret_cast<const float4*>(kv_smem + w * (STAGES * Tile::BYTES) + 4 * (i + 4 * h * D));
+        out.x = fmaf(x.x, f, out.x), out.y = fmaf(x.y, f, out.y);
+        out.z = fmaf(x.z, f, out.z), out.w = fmaf(x.w, f, out.w);
+      }
     *reinterpret_cast<float4*>(p.po + slot * (HEADS * D) + i) = out;
   }
   pos += tiles;
@@ -714,7 +759,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
     do {
       len = seq_len(a, ++b);  // pos < end: a sequence with tokens follows
     } while (len == 0);
-    item_tiles = (len + 15) / 16;
+    item_tiles = (len + TT - 1) / TT;
   }
   __syncthreads();  // the outputs in shared memory are read
   }
@@ -733,7 +778,7 @@ struct Parts {
 };
 __device__ __forceinline__ Parts item_parts(const Kv4Dev& p, int64_t b, int32_t in_seq, int32_t len) {
   const int64_t per = p.line[p.a.batch + 1], item = b * p.a.h_kv * p.chunks + in_seq;
-  const int64_t tiles = (len + 15) / 16, start = p.line[b] + in_seq * tiles;
+  const int64_t tiles = (len + p.tile - 1) / p.tile, start = p.line[b] + in_seq * tiles;
   return Parts{item + start / per, item + (start + tiles - 1) / per};
 }
 
@@ -857,8 +902,8 @@ cudaError_t launch_kv4_store(const Kv4StoreArgs& a, cudaStream_t st) {
 }
 
 // CTAs of the decode step: as many as stay resident, two per SM (one with 16 heads' outputs in registers).
-static int64_t kv4_grid(int64_t items, int64_t cap, bool one) {
-  return std::min<int64_t>(one ? 2 * 148 : 148, items * ((cap + 15) / 16));
+static int64_t kv4_grid(int64_t items, int64_t tiles, bool one) {
+  return std::min<int64_t>(one ? 2 * 148 : 148, items * tiles);
 }
 
 Kv4Ws kv4_ws(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, bool weights) {
@@ -867,7 +912,8 @@ Kv4Ws kv4_ws(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, b
   w.chunk_heads = group <= 8 ? 8 : 16;
   w.chunks = (group + w.chunk_heads - 1) / w.chunk_heads;
   const int64_t items = batch * h_kv * w.chunks;
-  w.grid = kv4_grid(items, cap, w.chunk_heads == 8);
+  w.tile = group <= 4 ? 32 : 16;
+  w.grid = kv4_grid(items, (cap + w.tile - 1) / w.tile, w.chunk_heads == 8);
   const int64_t rows = (w.grid + items) * w.chunk_heads;
   auto al = [](int64_t x) { return (x + 1023) / 1024 * 1024; };
   int64_t off = 1024;
@@ -884,13 +930,20 @@ Kv4Ws kv4_ws(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, b
 }
 
 namespace {
-template <int NG, int NT>
+template <int NG, int NT, int HALVES>
 cudaError_t launch_split(const Kv4Dev& p, const Kv4Ws& w, cudaStream_t st) {
-  constexpr int smem = kKvWarps * kKvStages * KvTile<NG>::BYTES;
-  cudaError_t e = cudaFuncSetAttribute(kv4_attn_split_kernel<NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  using Tile = KvTile<NG, HALVES>;
+  constexpr int smem = kKvWarps * Tile::STAGES * Tile::BYTES;
+  cudaError_t e =
+      cudaFuncSetAttribute(kv4_attn_split_kernel<NG, NT, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_attn_split_kernel<NG, NT>, dim3(unsigned(w.grid)), dim3(kKvWarps * 32), size_t(smem), st,
+  return launch_pdl(kv4_attn_split_kernel<NG, NT, HALVES>, dim3(unsigned(w.grid)), dim3(kKvWarps * 32), size_t(smem), st,
                     dim3(0, 0, 0), p);
+}
+template <int NG>
+cudaError_t launch_split(const Kv4Dev& p, const Kv4Ws& w, cudaStream_t st) {
+  if (w.tile == 32) return launch_split<NG, 1, 2>(p, w, st);
+  return w.chunk_heads == 8 ? launch_split<NG, 1, 1>(p, w, st) : launch_split<NG, 2, 1>(p, w, st);
 }
 }  // namespace
 
@@ -905,13 +958,13 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st) {
   p.line = reinterpret_cast<int64_t*>(base + w.line);
   p.chunks = int32_t(w.chunks);
   p.chunk_heads = int32_t(w.chunk_heads);
+  p.tile = int32_t(w.tile);
   cudaError_t e;
-  const bool one = w.chunk_heads == 8;
   switch (a.d / kKv4Group) {
-    case 1: e = one ? launch_split<1, 1>(p, w, st) : launch_split<1, 2>(p, w, st); break;
-    case 2: e = one ? launch_split<2, 1>(p, w, st) : launch_split<2, 2>(p, w, st); break;
-    case 3: e = one ? launch_split<3, 1>(p, w, st) : launch_split<3, 2>(p, w, st); break;
-    default: e = one ? launch_split<4, 1>(p, w, st) : launch_split<4, 2>(p, w, st); break;
+    case 1: e = launch_split<1>(p, w, st); break;
+    case 2: e = launch_split<2>(p, w, st); break;
+    case 3: e = launch_split<3>(p, w, st); break;
+    default: e = launch_split<4>(p, w, st); break;
   }
   if (e != cudaSuccess) return e;
   const int64_t o_blocks = a.batch * a.h_q;

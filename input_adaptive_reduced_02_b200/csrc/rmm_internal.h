@@ -299,6 +299,7 @@ cudaError_t launch_kv4_store(const Kv4StoreArgs& a, cudaStream_t st);
 // Workspace of one decode call, in bytes from its 1 KiB-aligned base.
 struct Kv4Ws {
   int64_t grid, chunks, chunk_heads;  // CTAs; chunks of a key head's query heads, and their size
+  int64_t tile;                       // tokens of a tile
   size_t line, ml, o, scores, bytes;
 };
 Kv4Ws kv4_ws(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, bool weights);
