@@ -533,10 +533,13 @@ size_t rmm_kv4_attn_workspace_size(int64_t batch, int64_t h_q, int64_t h_kv, int
  * gets O = 0 and lse = -inf. lse: nullable f32 [batch][h_q]. w_out (nullable,
  * f32 [batch][h_kv][cap]): w_out[b][h][t] = w_in[b][h][t] + the probabilities
  * of token t summed over the query heads that read head h, for t < lens[b]; w_in
- * NULL counts as zeros and may be w_out. The probabilities (times the values'
- * steps) are rounded to bf16 for the product, sums are f32 in a fixed order.
+ * NULL counts as zeros and may be w_out. The probabilities times the values'
+ * steps are rounded to f16 for the product, sums are f32 in a fixed order.
  * Workspace 1 KiB-aligned, its first word the status word (rmm_check), cleared
- * at the start. Slots at and past lens[b] are not used. */
+ * at the start; RMM_STATUS_BIT_NONFINITE: a head's sum is not a positive finite
+ * number. Slots at and past lens[b] are not used. Queries beyond 2^100 may
+ * overflow (infinite or NaN results); a probability times step 2^-29 or more
+ * below the sequence's largest loses bits of its own. */
 rmm_status rmm_kv4_attn(const void* Q, int64_t q_ss, int64_t q_hs, const uint8_t* kc, const void* ks,
                         const uint8_t* vc, const void* vs, const int32_t* lens, int64_t batch, int64_t h_q,
                         int64_t h_kv, int64_t d, int64_t cap, float scale, rmm_dtype in, void* O, int64_t o_ss,

@@ -191,10 +191,12 @@ __device__ __forceinline__ int32_t seq_len(const Kv4AttnArgs& a, int64_t b) {
 //       bits fit f16 exactly over 28 binades below it. One accumulator per
 //       group of 32 channels, then S += step·acc in f32; min·(sum of q) of all
 //       groups is one more product, the sums cut into three bf16 parts.
-//   Oᵀ  A = codes of 16 channels as bf16 subnormals c·2^-133 or 16c·2^-133, B =
-//       2^64·p·step of the group in bf16, transposed by movmatrix; p·min adds
-//       up in f32. The 2^64 keeps the products normal f32 numbers for p·step
-//       from 2^-57 (smaller ones fade out) up to 2^62.
+//   Oᵀ  A = codes of 16 channels, the same f16 subnormals, B = p·step of the
+//       group in f16, transposed by movmatrix; p·min adds up in f32. A power of
+//       two per warp, raised as larger steps come (and O with it), keeps p·step
+//       below 2^15: 11 bits where bf16 would keep 8, which matters since a value
+//       is the small difference of its min and step·code (bf16: twice the error
+//       of the result). What lies 2^-29 below the largest p·step fades out.
 // So a word of 8 codes costs one shift and four masks. What bounds the kernel
 // is the rate of such instructions, then HBM.
 // With up to 4 query heads per key head a tile has two halves of 16 tokens: the
@@ -510,6 +512,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   }
 
   float o[NT][2 * NG][4], om[NT][NG][2], nm[NT][2], l[NT][2];
+  uint32_t v_exp = 127, step_lim = 0;  // exponent of the power of two; steps (bf16 bits) it is good for: none yet
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -605,8 +608,21 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
         pr[n][c] = fmaf(t[n][c], fh[n][c & 1], nm[n][c & 1]);
         top = fmaxf(top, pr[n][c]);
       }
+    uint32_t top_step = 0;  // of this lane's share of the values' steps
+    constexpr int WORDS = TT * NG;
+#pragma unroll
+    for (int i = 0; i < (WORDS + 31) / 32; ++i)
+      top_step = max(top_step, reinterpret_cast<const uint32_t*>(vs)[(lane + 32 * i) % WORDS] & 0x7FFFu);
     const bool tail = TT * tile + TT > rows;
-    if (__any_sync(0xffffffffu, tail || top > kKvRescale)) {
+    if (__any_sync(0xffffffffu, tail || top > kKvRescale || top_step > step_lim)) {
+      top_step = __reduce_max_sync(0xffffffffu, top_step);
+      float fv = 1.f;
+      if (top_step > step_lim) {  // the largest step becomes 2^5 to 2^6, one binade more is let through
+        const uint32_t e = top_step >> 7, next = min(max(259 - int32_t(e), 1), 254);
+        if (step_lim > 0) fv = __uint_as_float(uint32_t(max(127 + int32_t(next) - int32_t(v_exp), 0)) << 23);
+        v_exp = next;
+        step_lim = (e + 1) << 7 | 0x7Fu;
+      }
       if (tail) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -631,8 +647,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
             om[n][g][x] *= f;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              o[n][2 * g + u][x] *= f;
-              o[n][2 * g + u][2 + x] *= f;
+              o[n][2 * g + u][x] *= f * fv;
+              o[n][2 * g + u][2 + x] *= f * fv;
             }
           }
           pr[n][x] = t[n][x] == -INFINITY ? -INFINITY : fmaf(t[n][x], fh[n][x], nm2);
@@ -647,11 +663,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       l[n][1] += pr[n][1] + pr[n][3];
     }
     // ---- values
+    const float up = __uint_as_float(v_exp << 23);
     float big[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) big[n][c] = pr[n][c] * 0x1p64f;
+      for (int c = 0; c < 4; ++c) big[n][c] = pr[n][c] * up;
     uint32_t wl[HALVES][NG], wh[HALVES][NG], s0[NG], s1[NG];
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
@@ -667,8 +684,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       uint32_t b0[NT], b1[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        b0[n] = movmatrix_trans(pack_bf16x2(big[n][0] * st0, big[n][1] * st0));
-        b1[n] = movmatrix_trans(pack_bf16x2(big[n][2] * st1, big[n][3] * st1));
+        b0[n] = movmatrix_trans(pack_f16x2(big[n][0] * st0, big[n][1] * st0));
+        b1[n] = movmatrix_trans(pack_f16x2(big[n][2] * st1, big[n][3] * st1));
         om[n][g][0] = fmaf(pr[n][0], mn0, fmaf(pr[n][2], mn1, om[n][g][0]));
         om[n][g][1] = fmaf(pr[n][1], mn0, fmaf(pr[n][3], mn1, om[n][g][1]));
       }
@@ -680,8 +697,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
         const uint32_t cols = HALVES == 1 || r >> 2 == h ? 0xFFFFFFFFu : 0u;  // column r's half
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma_bf16(o[n][2 * g], av[0], b0[n] & cols, b1[n] & cols);
-          mma_bf16(o[n][2 * g + 1], av[1], b0[n] & cols, b1[n] & cols);
+          mma_f16(o[n][2 * g], av[0], b0[n] & cols, b1[n] & cols);
+          mma_f16(o[n][2 * g + 1], av[1], b0[n] & cols, b1[n] & cols);
         }
       }
     }
@@ -708,6 +725,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       }
     }
   float* mine = reinterpret_cast<float*>(ring);  // [HEADS][D]
+  const float down = __uint_as_float((254u - v_exp) << 23);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -717,7 +735,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           mine[(8 * n + 2 * j + (c & 1)) * D + 32 * g + 16 * u + 8 * (c >> 1) + r] =
-              fmaf(o[n][2 * g + u][c], c < 2 ? 0x1p69f : 0x1p65f, om[n][g][c & 1]);
+              fmaf(o[n][2 * g + u][c] * (c < 2 ? 0x1p24f : 0x1p20f), down, om[n][g][c & 1]);
   __syncthreads();
   if (tid < heads) {  // m_sh becomes the warps' factors (a head's second column: of the second half)
     float m = m_sh[0][tid];  // the first warp has a tile

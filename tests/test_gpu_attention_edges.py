@@ -117,6 +117,22 @@ def test_decode_of_values_of_any_size(mul):
     assert abs(lse[0, 0].item() - np.log(L)) < 1e-6
 
 
+def test_decode_of_values_that_grow_along_the_sequence():
+    """Steps from 2^-2 up to 2^28 and back, the probabilities of the small ones near 1 in some heads."""
+    L, hq, hk, d = 400, 8, 2, 64
+    cache = rmm.KV4Cache.empty(1, hk, L, d)
+    t = torch.arange(L, device=DEV)
+    grow = torch.exp2(torch.minimum(t, L - t).float() / 7).view(L, 1, 1)
+    K, V = randn(L, hk, d, seed=1).float(), randn(L, hk, d, seed=2).float() * grow
+    K[7] += 6.0  # a token of small values that takes most of the weight where the query is positive
+    rmm.kv4_store(cache, K, V, i32([0]), i32([0, L]))
+    Q = randn(1, hq, d, seed=3, mul=0.2)
+    Q[0, ::2] = Q[0, ::2].abs()
+    O, lse, ws = rmm.kv4_attn(Q, cache, i32([L]))
+    rmm.check(ws)
+    check_decode(Q, cache, [L], O, lse, d ** -0.5)
+
+
 def test_decode_reports_nan_scales():
     cache = filled_cache([40, 40], 64, 1, 64, seed=1)
     cache.ks[1, 0, 17] = float("nan")
