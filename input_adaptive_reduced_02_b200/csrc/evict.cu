@@ -296,7 +296,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictPlane& 
 // IN_PLACE: some plane is. Without that path six blocks fit an SM, which moves
 // 290 MB of 4-bit rows in 52 us instead of 57 us.
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 4 : 6)
+__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 3 : 6)
 evict_move_kernel(const EvictArgs a, const MovePlan plan) {
   __shared__ int32_t from[kMoveRows];
   pdl_trigger();

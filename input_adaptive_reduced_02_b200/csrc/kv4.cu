@@ -786,9 +786,10 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
 // Joins the parts of each item. Blocks [0, batch·h_q): O and the log-sum-exp of
 // one head. The rest, w_out = w_in + the group's probabilities, kJoinTokens
 // each; their scores are on the way while the parts' sums are joined.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinEach = 4;  // tokens of a thread
+constexpr int kJoinThreads = 128;
+constexpr int kJoinEach = 8;  // tokens of a thread
 constexpr int kJoinTokens = kJoinThreads * kJoinEach;
+constexpr int kJoinParts = 8;  // parts of an item on the way at once
 
 // The slots of an item's parts: [first, last].
 struct Parts {
@@ -797,7 +798,7 @@ struct Parts {
 __device__ __forceinline__ Parts item_parts(const Kv4Dev& p, int64_t b, int32_t in_seq, int32_t len) {
   const int64_t per = p.line[p.a.batch + 1], item = b * p.a.h_kv * p.chunks + in_seq;
   const int64_t tiles = (len + p.tile - 1) / p.tile, start = p.line[b] + in_seq * tiles;
-  return Parts{item + start / per, item + (start + tiles - 1) / per};
+  return Parts{item + div_up(start + 1, per) - 1, item + div_up(start + tiles, per) - 1};
 }
 
 // maximum and sum over the parts of one head (log2 units): every lane gets both
@@ -809,7 +810,7 @@ __device__ __forceinline__ float2 join_ml(const Kv4Dev& p, Parts s, int32_t head
   float l = 0.f;
   for (int64_t i = s.first + lane; i <= s.last; i += 32) {
     const float2 x = reinterpret_cast<const float2*>(p.ml)[i * p.chunk_heads + head];
-    l += x.y * exp2f(x.x - m);
+    l += x.y * ex2f(x.x - m);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -829,34 +830,50 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
     const int64_t b = blockIdx.x / a.h_q, hq = blockIdx.x % a.h_q;
     const int32_t len = seq_len(a, b);
     const int32_t hg = int32_t(hq % gq), head = hg % p.chunk_heads;
-    const Parts parts = item_parts(p, b, int32_t(hq / gq) * p.chunks + hg / p.chunk_heads, len);
-    float2 g = make_float2(-INFINITY, 0.f);
-    if (len > 0) g = join_ml(p, parts, head, lane);
-    if (tid == 0) {
-      if (len > 0 && !(g.y > 0.f && g.y < INFINITY && isfinite(g.x)))
-        status_or(static_cast<uint32_t*>(a.workspace), RMM_NONFINITE_BIT);
-      if (a.lse) a.lse[b * a.h_q + hq] = len > 0 ? (g.x + log2f(g.y)) * 0.6931471805599453f : -INFINITY;
-    }
-    if (tid < a.d) {
-      float o = 0.f;
-      if (len > 0) {
-#pragma unroll 4
-        for (int64_t i = parts.first; i <= parts.last; ++i) {
-          const int64_t at = i * p.chunk_heads + head;
-          o += p.po[at * a.d + tid] * exp2f(p.ml[2 * at] - g.x);
-        }
-        o /= g.y;
+    const Parts parts =
+        len > 0 ? item_parts(p, b, int32_t(hq / gq) * p.chunks + hg / p.chunk_heads, len) : Parts{0, -1};
+    // a thread per channel; all of them add up the parts' sums
+    if (tid >= a.d) return;
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    for (int64_t i = parts.first; len > 0 && i <= parts.last; i += kJoinParts) {
+      float2 x[kJoinParts];
+      float v[kJoinParts];
+#pragma unroll
+      for (int u = 0; u < kJoinParts; ++u) {
+        const int64_t at = min(i + u, parts.last) * p.chunk_heads + head;
+        x[u] = reinterpret_cast<const float2*>(p.ml)[at];
+        v[u] = p.po[at * a.d + tid];
       }
-      const int64_t at = b * a.o_ss + hq * a.o_hs + tid;
-      if (a.out == kBF16)
-        static_cast<uint16_t*>(a.o)[at] = uint16_t(pack_bf16x2(o, 0.f));
-      else
-        static_cast<float*>(a.o)[at] = o;
+      float mx = m;
+#pragma unroll
+      for (int u = 0; u < kJoinParts; ++u) mx = fmaxf(mx, x[u].x);
+      const float f = ex2f(m - mx);
+      l *= f;
+      o *= f;
+#pragma unroll
+      for (int u = 0; u < kJoinParts; ++u) {
+        if (i + u > parts.last) break;
+        const float e = ex2f(x[u].x - mx);
+        l = fmaf(x[u].y, e, l);
+        o = fmaf(v[u], e, o);
+      }
+      m = mx;
     }
+    if (tid == 0) {
+      if (len > 0 && !(l > 0.f && l < INFINITY && isfinite(m)))
+        status_or(static_cast<uint32_t*>(a.workspace), RMM_NONFINITE_BIT);
+      if (a.lse) a.lse[b * a.h_q + hq] = len > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+    o = len > 0 ? o / l : 0.f;
+    const int64_t at = b * a.o_ss + hq * a.o_hs + tid;
+    if (a.out == kBF16)
+      static_cast<uint16_t*>(a.o)[at] = uint16_t(pack_bf16x2(o, 0.f));
+    else
+      static_cast<float*>(a.o)[at] = o;
     return;
   }
-  const int64_t i = blockIdx.x - o_blocks;
-  const int64_t pieces = (a.cap + kJoinTokens - 1) / kJoinTokens;
+  const int32_t i = int32_t(blockIdx.x - o_blocks);
+  const int32_t pieces = int32_t((a.cap + kJoinTokens - 1) / kJoinTokens);
   const int64_t item = i / pieces;
   const int64_t b = item / a.h_kv, h = item % a.h_kv;
   const int32_t len = seq_len(a, b);
@@ -888,9 +905,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
     float s = 0.f;
     if constexpr (GV > 0) {
 #pragma unroll
-      for (int g = 0; g < GV; ++g) s += exp2f(x[e][g] - lse2[g]);
+      for (int g = 0; g < GV; ++g) s += ex2f(x[e][g] - lse2[g]);
     } else {
-      for (int g = 0; g < gq; ++g) s += exp2f(p.scores[at * gq + g] - lse2[g]);
+      for (int g = 0; g < gq; ++g) s += ex2f(p.scores[at * gq + g] - lse2[g]);
     }
     a.w_out[at] = w[e] + s;
   }
