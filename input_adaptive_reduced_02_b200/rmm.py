@@ -646,7 +646,7 @@ def _tokens(t: torch.Tensor, name: str):
 
 
 def _i32_vec(t: torch.Tensor, name: str, n: int, device):
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.numel() != n:
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements on {device}")
     return t
 
@@ -662,7 +662,8 @@ def _packed(Q: torch.Tensor, K: torch.Tensor, cu_q, cu_k):
     """Sizes and strides of packed queries and keys, and the number of sequences."""
     T_q, h_q, d, q_ts, q_hs = _tokens(Q, "Q")
     T_k, h_kv, dk, k_ts, k_hs = _tokens(K, "K")
-    if dk != d or K.device != Q.device or K.dtype != Q.dtype:
+    device = Q.device
+    if dk != d or K.device != device or K.dtype != Q.dtype:
         raise ValueError("Q and K disagree on d, dtype or device")
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k go together")
@@ -670,8 +671,8 @@ def _packed(Q: torch.Tensor, K: torch.Tensor, cu_q, cu_k):
     if n < 0:
         raise ValueError("cu_q must hold n_seq + 1 boundaries")
     if cu_q is not None:
-        _i32_vec(cu_q, "cu_q", n + 1, Q.device)
-        _i32_vec(cu_k, "cu_k", n + 1, Q.device)
+        _i32_vec(cu_q, "cu_q", n + 1, device)
+        _i32_vec(cu_k, "cu_k", n + 1, device)
     return T_q, T_k, h_q, h_kv, d, q_ts, q_hs, k_ts, k_hs, n
 
 
@@ -687,23 +688,26 @@ def attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.T
     O [T_q][h_q][d]; lse f32 [h_q][T_q]."""
     T_q, T_k, h_q, h_kv, d, q_ts, q_hs, k_ts, k_hs, n = _packed(Q, K, cu_q, cu_k)
     tv, hv, dv, v_ts, v_hs = _tokens(V, "V")
-    if (tv, hv, dv) != (T_k, h_kv, d) or V.device != Q.device or V.dtype != Q.dtype:
+    device = Q.device
+    if tv != T_k or hv != h_kv or dv != d or V.device != device or V.dtype != Q.dtype:
         raise ValueError("K and V disagree on shape, dtype or device")
     if out is None:
-        out = torch.empty(T_q, h_q, d, dtype=out_dtype, device=Q.device)
+        out = torch.empty(T_q, h_q, d, dtype=out_dtype, device=device)
         o_ts, o_hs = h_q * d, d
-    elif tuple(out.shape) != (T_q, h_q, d) or out.device != Q.device:
+    elif out.shape != (T_q, h_q, d) or out.device != device:
         raise ValueError("out must be [T_q][h_q][d] on Q's device")
     else:
         _, _, _, o_ts, o_hs = _tokens(out, "out")
     if lse is None:
-        lse = torch.empty(h_q, T_q, dtype=torch.float32, device=Q.device)
+        lse = torch.empty(h_q, T_q, dtype=torch.float32, device=device)
     else:
-        _f32_shape(lse, "lse", (h_q, T_q), Q.device)
-    _check(lib().rmm_attn_prompt(_ptr(Q), q_ts, q_hs, _ptr(K), k_ts, k_hs, _ptr(V), v_ts, v_hs, _ptr(cu_q),
-                                 _ptr(cu_k), n, T_q, T_k, h_q, h_kv, d, float(d ** -0.5 if scale is None else scale),
-                                 int(causal), _dtype(Q), _ptr(out), o_ts, o_hs, _out_code(out.dtype), _ptr(lse),
-                                 _ptr(status), _stream(Q)))
+        _f32_shape(lse, "lse", (h_q, T_q), device)
+    status_code = lib().rmm_attn_prompt(
+        Q.data_ptr(), q_ts, q_hs, K.data_ptr(), k_ts, k_hs, V.data_ptr(), v_ts, v_hs, _ptr(cu_q), _ptr(cu_k), n, T_q, T_k,
+        h_q, h_kv, d, d ** -0.5 if scale is None else scale, causal, _dtype(Q), out.data_ptr(), o_ts, o_hs,
+        _out_code(out.dtype), lse.data_ptr(), _ptr(status), _stream(Q))
+    if status_code:
+        _check(status_code)
     return out, lse
 
 
@@ -737,18 +741,20 @@ class KV4Cache:
 
     def __init__(self, kc: torch.Tensor, ks: torch.Tensor, vc: torch.Tensor, vs: torch.Tensor,
                  w: torch.Tensor | None = None):
-        if kc.dim() != 4 or kc.dtype != torch.uint8 or not kc.is_cuda:
+        codes, device = kc.shape, kc.device
+        if len(codes) != 4 or kc.dtype != torch.uint8 or not kc.is_cuda:
             raise ValueError("kc must be a [batch][heads][cap][d/2] uint8 CUDA tensor")
-        self.batch, self.heads, self.cap, half = kc.shape
+        self.batch, self.heads, self.cap, half = codes
         self.d = 2 * half
         scales = (self.batch, self.heads, self.cap, self.d // KV4_GROUP, 2)
-        device = kc.device
-        for name, t, dt, shape in (("kc", kc, torch.uint8, kc.shape), ("vc", vc, torch.uint8, kc.shape),
-                                   ("ks", ks, torch.bfloat16, scales), ("vs", vs, torch.bfloat16, scales)):
-            if t.dtype != dt or t.shape != shape or not t.is_contiguous() or t.device != device:
-                raise ValueError(f"{name} must be a contiguous {dt} {list(shape)} tensor on {device}")
+        if not (vc.dtype == torch.uint8 and ks.dtype == torch.bfloat16 and vs.dtype == torch.bfloat16
+                and vc.shape == codes and ks.shape == scales and vs.shape == scales and kc.is_contiguous()
+                and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous() and vc.device == device
+                and ks.device == device and vs.device == device):
+            raise ValueError(f"kc, vc must be contiguous uint8 {list(codes)} and ks, vs contiguous bfloat16 "
+                             f"{list(scales)} tensors on {device}")
         self.kc, self.ks, self.vc, self.vs = kc, ks, vc, vs
-        self.w = _f32_shape(w, "w", (self.batch, self.heads, self.cap), device)
+        self.w = None if w is None else _f32_shape(w, "w", (self.batch, self.heads, self.cap), device)
 
     @classmethod
     def empty(cls, batch: int, heads: int, cap: int, d: int, device="cuda", weights: bool = True) -> "KV4Cache":
@@ -775,18 +781,22 @@ def kv4_store(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, start: torch.Te
     w_new [heads][T], or to 0."""
     T, h, d, k_ts, k_hs = _tokens(K, "K")
     tv, hv, dv, v_ts, v_hs = _tokens(V, "V")
-    if (tv, hv, dv) != (T, h, d) or (h, d) != (cache.heads, cache.d) or V.dtype != K.dtype:
+    if tv != T or hv != h or dv != d or h != cache.heads or d != cache.d or V.dtype != K.dtype:
         raise ValueError("K, V and the cache disagree on shape or dtype")
-    if K.device != cache.kc.device or V.device != K.device:
+    kc, batch, device = cache.kc, cache.batch, K.device
+    if kc.device != device or V.device != device:
         raise ValueError("K, V and the cache must be on one device")
-    _i32_vec(start, "start", cache.batch, K.device)
+    _i32_vec(start, "start", batch, device)
     if cu is not None:
-        _i32_vec(cu, "cu", cache.batch + 1, K.device)
+        _i32_vec(cu, "cu", batch + 1, device)
     if w_new is not None:
-        _f32_shape(w_new, "w_new", (h, T), K.device)
-    _check(lib().rmm_kv4_store(_ptr(K), k_ts, k_hs, _ptr(V), v_ts, v_hs, _dtype(K), _ptr(cu), _ptr(start),
-                               cache.batch, T, h, d, cache.cap, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc),
-                               _ptr(cache.vs), _ptr(w_new), _ptr(cache.w), _ptr(status), _stream(K)))
+        _f32_shape(w_new, "w_new", (h, T), device)
+    status_code = lib().rmm_kv4_store(
+        K.data_ptr(), k_ts, k_hs, V.data_ptr(), v_ts, v_hs, _dtype(K), _ptr(cu), start.data_ptr(), batch, T, h, d,
+        cache.cap, kc.data_ptr(), cache.ks.data_ptr(), cache.vc.data_ptr(), cache.vs.data_ptr(), _ptr(w_new),
+        _ptr(cache.w), _ptr(status), _stream(K))
+    if status_code:
+        _check(status_code)
     return cache
 
 
@@ -804,30 +814,32 @@ def kv4_attn(Q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, scale: float 
     the tokens' probabilities, summed over the query heads of their head, are
     added to w_in (None: 0) and written to w_out, which may be w_in."""
     n, h_q, d, q_ss, q_hs = _tokens(Q, "Q")
-    if n != cache.batch or d != cache.d or Q.device != cache.kc.device:
+    kc, heads, cap, device = cache.kc, cache.heads, cache.cap, Q.device
+    if n != cache.batch or d != cache.d or kc.device != device:
         raise ValueError("Q and the cache disagree on batch, d or device")
-    _i32_vec(lens, "lens", n, Q.device)
+    _i32_vec(lens, "lens", n, device)
     if w_in is not None:
-        _f32_shape(w_in, "w_in", (n, cache.heads, cache.cap), Q.device)
+        _f32_shape(w_in, "w_in", (n, heads, cap), device)
     if w_out is not None:
-        _f32_shape(w_out, "w_out", (n, cache.heads, cache.cap), Q.device)
-    ws = _ensure_ws(workspace, kv4_attn_workspace_size(n, h_q, cache.heads, d, cache.cap, w_out is not None), Q.device)
+        _f32_shape(w_out, "w_out", (n, heads, cap), device)
+    ws = _ensure_ws(workspace, kv4_attn_workspace_size(n, h_q, heads, d, cap, w_out is not None), device)
     if out is None:
-        out = torch.empty(n, h_q, d, dtype=out_dtype, device=Q.device)
+        out = torch.empty(n, h_q, d, dtype=out_dtype, device=device)
         o_ss, o_hs = h_q * d, d
-    elif tuple(out.shape) != (n, h_q, d) or out.device != Q.device:
+    elif out.shape != (n, h_q, d) or out.device != device:
         raise ValueError("out must be [batch][h_q][d] on Q's device")
     else:
         _, _, _, o_ss, o_hs = _tokens(out, "out")
     if lse is None:
-        lse = torch.empty(n, h_q, dtype=torch.float32, device=Q.device)
+        lse = torch.empty(n, h_q, dtype=torch.float32, device=device)
     else:
-        _f32_shape(lse, "lse", (n, h_q), Q.device)
-    _check(lib().rmm_kv4_attn(_ptr(Q), q_ss, q_hs, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs),
-                              _ptr(lens), n, h_q, cache.heads, d, cache.cap,
-                              float(d ** -0.5 if scale is None else scale), _dtype(Q), _ptr(out), o_ss, o_hs,
-                              _out_code(out.dtype), _ptr(lse), _ptr(w_in), _ptr(w_out), ws.ptr,
-                              ws.nbytes, _stream(Q)))
+        _f32_shape(lse, "lse", (n, h_q), device)
+    status_code = lib().rmm_kv4_attn(
+        Q.data_ptr(), q_ss, q_hs, kc.data_ptr(), cache.ks.data_ptr(), cache.vc.data_ptr(), cache.vs.data_ptr(),
+        lens.data_ptr(), n, h_q, heads, d, cap, d ** -0.5 if scale is None else scale, _dtype(Q), out.data_ptr(), o_ss,
+        o_hs, _out_code(out.dtype), lse.data_ptr(), _ptr(w_in), _ptr(w_out), ws.ptr, ws.nbytes, _stream(Q))
+    if status_code:
+        _check(status_code)
     return out, lse, ws
 
 
@@ -849,19 +861,18 @@ def cache_evict(w: torch.Tensor, lens: torch.Tensor, planes, budget: int, sink: 
     tokens' former indices, -1 past them. lens_out may be lens."""
     if w.dim() != 3 or w.dtype != torch.float32 or not w.is_cuda or not w.is_contiguous():
         raise ValueError("w must be a contiguous float32 [batch][heads][cap] CUDA tensor")
-    batch, heads, cap = w.shape
-    _i32_vec(lens, "lens", batch, w.device)
-    head, device = (batch, heads, cap), w.device
+    head, device, budget = w.shape, w.device, int(budget)
+    batch, heads, cap = head
+    _i32_vec(lens, "lens", batch, device)
     cap_out, vals = None, []
     for i, pair in enumerate(planes):
         src, dst = pair if isinstance(pair, tuple) else (pair, pair)
         shape, out_shape = src.shape, dst.shape
         if cap_out is None and len(out_shape) >= 3:
             cap_out = out_shape[2]
-        if (len(shape) < 3 or shape[:3] != head or src.dtype != dst.dtype or not src.is_contiguous()
-                or src.device != device or (dst is not src and (
-                    out_shape != (batch, heads, cap_out, *shape[3:]) or not dst.is_contiguous()
-                    or dst.device != device)) or (dst is src and cap_out != cap)):
+        if (len(shape) < 3 or (shape if len(shape) == 3 else shape[:3]) != head or src.dtype != dst.dtype or not src.is_contiguous() or src.device != device
+                or (cap_out != cap if dst is src else out_shape[:2] != head[:2] or out_shape[2:3] != (cap_out,)
+                    or out_shape[3:] != shape[3:] or not dst.is_contiguous() or dst.device != device)):
             raise ValueError(f"plane {i}: src and dst must be contiguous [batch][heads][cap][...] tensors like w, "
                              "the destinations of one capacity")
         row = src.element_size()
@@ -870,18 +881,22 @@ def cache_evict(w: torch.Tensor, lens: torch.Tensor, planes, budget: int, sink: 
         vals += (src.data_ptr(), dst.data_ptr(), row)
     n_planes = len(vals) // 3
     if cap_out is None:
-        cap_out = max(cap, int(budget))
+        cap_out = max(cap, budget)
     arr = (ctypes.c_int64 * max(3, len(vals)))(*vals)  # rmm_cache_plane: two pointers and the row's bytes
     if lens_out is None:
-        lens_out = torch.empty(batch, dtype=torch.int32, device=w.device)
-    _i32_vec(lens_out, "lens_out", batch, w.device)
+        lens_out = torch.empty(batch, dtype=torch.int32, device=device)
+    else:
+        _i32_vec(lens_out, "lens_out", batch, device)
     if idx_out is None:
-        idx_out = torch.empty(batch, heads, int(budget), dtype=torch.int32, device=w.device)
-    _i32_vec(idx_out, "idx_out", batch * heads * int(budget), w.device)
-    ws = _ensure_ws(workspace, cache_evict_workspace_size(batch, heads, int(budget)), w.device)
-    _check(lib().rmm_cache_evict(_ptr(w), _ptr(lens), batch, heads, cap, int(budget), int(sink), int(recent), arr,
-                                 n_planes, cap_out, _ptr(lens_out), _ptr(idx_out), ws.ptr,
-                                 ws.nbytes, _stream(w)))
+        idx_out = torch.empty(batch, heads, budget, dtype=torch.int32, device=device)
+    else:
+        _i32_vec(idx_out, "idx_out", batch * heads * budget, device)
+    ws = _ensure_ws(workspace, cache_evict_workspace_size(batch, heads, budget), device)
+    status_code = lib().rmm_cache_evict(
+        w.data_ptr(), lens.data_ptr(), batch, heads, cap, budget, int(sink), int(recent), arr, n_planes, cap_out,
+        lens_out.data_ptr(), idx_out.data_ptr(), ws.ptr, ws.nbytes, _stream(w))
+    if status_code:
+        _check(status_code)
     return lens_out, idx_out, ws
 
 
