@@ -817,7 +817,7 @@ __device__ __forceinline__ float2 join_ml(const Kv4Dev& p, Parts s, int32_t head
   return make_float2(m, l);
 }
 
-// GV: query heads per key head, where that is 4 or 8 (16-byte loads); else 0.
+// GV: query heads per key head where that is 1, 2, 4 or 8; else 0, and the scores are read when they are needed.
 template <int GV>
 __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4Dev p, int64_t o_blocks) {
   extern __shared__ float lse2[];  // [h_q / h_kv]
@@ -884,10 +884,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const Kv4De
   for (int e = 0; e < kJoinEach; ++e) {
     const int32_t t = min(t0 + e * kJoinThreads + tid, len - 1);
     const int64_t at = item * a.cap + t;
+    if constexpr (GV % 4 == 0) {
 #pragma unroll
-    for (int v = 0; v < GV / 4; ++v) {
-      const float4 u = reinterpret_cast<const float4*>(p.scores + at * GV)[v];
-      x[e][4 * v] = u.x, x[e][4 * v + 1] = u.y, x[e][4 * v + 2] = u.z, x[e][4 * v + 3] = u.w;
+      for (int v = 0; v < GV / 4; ++v) {
+        const float4 u = reinterpret_cast<const float4*>(p.scores + at * GV)[v];
+        x[e][4 * v] = u.x, x[e][4 * v + 1] = u.y, x[e][4 * v + 2] = u.z, x[e][4 * v + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < GV; ++v) x[e][v] = p.scores[at * GV + v];
     }
     w[e] = a.w_in ? a.w_in[at] : 0.f;
   }
@@ -1006,6 +1011,8 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st) {
   const int64_t w_blocks = a.w_out ? a.batch * a.h_kv * ((a.cap + kJoinTokens - 1) / kJoinTokens) : 0;
   const int64_t group = a.h_q / a.h_kv;
   const dim3 grid(unsigned(o_blocks + w_blocks)), block(kJoinThreads), none(0, 0, 0);
+  if (group == 1) return launch_pdl(kv4_attn_join_kernel<1>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
+  if (group == 2) return launch_pdl(kv4_attn_join_kernel<2>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
   if (group == 4) return launch_pdl(kv4_attn_join_kernel<4>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
   if (group == 8) return launch_pdl(kv4_attn_join_kernel<8>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
   return launch_pdl(kv4_attn_join_kernel<0>, grid, block, size_t(group) * 4, st, none, p, o_blocks);
