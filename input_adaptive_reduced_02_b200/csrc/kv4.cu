@@ -60,32 +60,45 @@ __device__ __forceinline__ void load8(float (&f)[8], const T* p, bool vec) {
   }
 }
 
-// The 8 codes of x, nibble e for x[e]: rint((x - mn) / step) within 0 .. 15.
-// The product with the reciprocal is within 2^-17 of the quotient (about -1 to
-// 17), so only where one lands next to a half, or where the reciprocal is no
-// normal number, are the divisions made.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float step, float mn) {
+// bf16(range / 15), the quotient IEEE's. The product with 1/15 is off by at most
+// two units in its last place, which matters next to the middle of two bf16
+// numbers only (and below the normal range).
+__device__ __forceinline__ float fifteenth(float range) {
+  const float q = range * (1.0f / 15.0f);
+  const uint32_t low = (__float_as_uint(q) & 0xFFFFu) - 0x7FFCu;
+  return low <= 8u || q < 0x1p-100f ? __fdiv_rn(range, 15.0f) : q;
+}
+
+// The 8 codes of x (channel pairs), nibble e for channel e: rint((x - mn) / step)
+// within 0 .. 15. The product with the approximate reciprocal is within 2^-17 of
+// the quotient (about -1 to 17), so only where one lands next to a half, or
+// where the reciprocal is no normal number, are the divisions made.
+__device__ __forceinline__ uint32_t codes_of(const float2 (&x)[4], float step, float mn) {
   if (!(step > 0.f)) return 0;
-  const float inv = 1.0f / step;
-  float r[8], far = 0.f;
+  auto both = [](float v) { return make_float2(v, v); };
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+  float2 r[4];
+  float far = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 4; ++e) {
     // the nearest integer, by an addition that leaves no bits below 1 (exact for quotients below 2^22)
-    const float q = (x[e] - mn) * inv;
-    r[e] = __fsub_rn(__fadd_rn(q, 12582912.f), 12582912.f);
-    far = fmaxf(far, fabsf(q - r[e]));
+    const float2 q = mul2(add2(x[e], both(-mn)), both(inv));
+    r[e] = add2(add2(q, both(12582912.f)), both(-12582912.f));
+    const float2 off = fma2(r[e], both(-1.f), q);
+    far = max3(far, fabsf(off.x), fabsf(off.y));
   }
   if (!(far < 0.5f - 0x1p-15f && step > 0x1p-120f && step < 0x1p120f)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = rintf(__fdiv_rn(x[e] - mn, step));
+    for (int e = 0; e < 4; ++e)
+      r[e] = make_float2(rintf(__fdiv_rn(x[e].x - mn, step)), rintf(__fdiv_rn(x[e].y - mn, step)));
   }
-  float acc[2] = {0.f, 0.f};  // four codes each as one number below 2^16
 #pragma unroll
-  for (int e = 3; e >= 0; --e) {
-    acc[0] = fmaf(acc[0], 16.f, fminf(fmaxf(r[e], 0.f), 15.f));
-    acc[1] = fmaf(acc[1], 16.f, fminf(fmaxf(r[4 + e], 0.f), 15.f));
-  }
-  return uint32_t(acc[0]) | uint32_t(acc[1]) << 16;
+  for (int e = 0; e < 4; ++e)
+    r[e] = make_float2(fminf(fmaxf(r[e].x, 0.f), 15.f), fminf(fmaxf(r[e].y, 0.f), 15.f));
+  // four codes as one number below 2^16
+  const float2 lo = fma2(r[1], both(256.f), r[0]), hi = fma2(r[3], both(256.f), r[2]);
+  return uint32_t(fmaf(lo.y, 16.f, lo.x)) | uint32_t(fmaf(hi.y, 16.f, hi.x)) << 16;
 }
 
 template <typename T, int NG>
@@ -114,22 +127,24 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
   bool odd = false;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    float lo = x[kv][0], hi = lo, zero = 0.f;  // zero: NaN where an element is NaN or infinite
+    float2 p[4], zero = make_float2(0.f, 0.f);  // zero: NaN where an element is NaN or infinite
+    float lo = x[kv][0], hi = lo;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[kv][e]);
-      hi = fmaxf(hi, x[kv][e]);
-      zero = fmaf(x[kv][e], 0.f, zero);
+    for (int e = 0; e < 4; ++e) {
+      p[e] = make_float2(x[kv][2 * e], x[kv][2 * e + 1]);
+      lo = min3(lo, p[e].x, p[e].y);
+      hi = max3(hi, p[e].x, p[e].y);
+      zero = fma2(p[e], make_float2(0.f, 0.f), zero);
     }
-    odd |= zero != 0.f;
+    odd |= zero.x + zero.y != 0.f;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     // (step, minimum) as stored; the IEEE quotient, so that it depends on nothing but the values
-    const uint32_t sm = pack_bf16x2(__fdiv_rn(hi - lo, 15.0f), lo);
-    const uint32_t codes = codes_of(x[kv], __uint_as_float(sm << 16), __uint_as_float(sm & 0xFFFF0000u));
+    const uint32_t sm = pack_bf16x2(fifteenth(hi - lo), lo);
+    const uint32_t codes = codes_of(p, __uint_as_float(sm << 16), __uint_as_float(sm & 0xFFFF0000u));
     // the values' half-words need one nibble from each of the group's four lanes
     uint32_t half[2] = {0u, 0u};  // half-words r = 2j, 2j + 1 of group w
     if (kv == 1) {
