@@ -380,7 +380,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const bool row_ok = r < p.nq_tile * p.g && q < S_q;
       const int32_t lim = row_ok ? (a.causal ? min(S_k, q + off + 1) : S_k) : S_k;  // idle rows: anything
       const float c = a.scale * kLog2e;
-      float m = -INFINITY, nm = 0.f, l = 0.f;  // maximum of s; -(maximum·c) (0 while there is none); sum
+      // Maximum of s; -(maximum·c) (0 while there is none); sum. An idle row holds whatever shared memory
+      // or the next sequence's queries do: above every score, it never votes for a rescaling, which
+      // would round the live rows' P under another maximum.
+      float m = row_ok ? -INFINITY : INFINITY, nm = 0.f, l = 0.f;
       bool ok = true;
       for (int32_t j = 0; j < nk[t]; ++j) {
         if (!warp_wait(&s_full[t], uint32_t(j) & 1u, limit, abort_v)) {
