@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       top_step = __reduce_max_sync(0xffffffffu, top_step);
       float fv = 1.f;
       if (top_step > step_lim) {  // the largest step becomes 2^5 to 2^6, one binade more is let through
-        const uint32_t e = top_step >> 7, next = min(max(259 - int32_t(e), 1), 254);
+        // at most 2^119: p up to 2^8 times it is finite, and its reciprocal a normal number
+        const uint32_t e = top_step >> 7, next = min(max(259 - int32_t(e), 1), 246);
         if (step_lim > 0) fv = __uint_as_float(uint32_t(max(127 + int32_t(next) - int32_t(v_exp), 0)) << 23);
         v_exp = next;
         step_lim = (e + 1) << 7 | 0x7Fu;

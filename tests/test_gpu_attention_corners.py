@@ -1,5 +1,5 @@
 """The attention operators where a value, a size or a neighbour is unusual: rows
-that a tile leaves idle. Tolerances as derived in test_gpu_attention.py unless a
+that a tile leaves idle, steps next to nothing. Tolerances as derived in test_gpu_attention.py unless a
 test derives its own."""
 from __future__ import annotations
 
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from input_adaptive_reduced_02_b200 import rmm
-from test_gpu_attention import DEV, check_prompt, make_prompt
+from test_gpu_attention import DEV, check_decode, check_prompt, cum, i32, make_prompt, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,32 @@ def test_a_sequence_has_the_same_bits_alone_and_packed(hq, hk, d):
     Q[50:] = float("nan")  # unread by the first sequence in any form
     O, lse = rmm.attn_prompt(Q, K, V, cq, ck)
     assert torch.equal(O[:50], alone[0]) and torch.equal(lse[:, :50], alone[1])
+
+
+# ---------------------------------------------------------------- steps of the decode's values
+def growing_scores(n, L, hq, hk, d, log2_per_256):
+    """Queries and keys whose scores grow along the sequence by so many powers of two per 256 tokens, a little uneven."""
+    K, Q = randn(n * L, hk, d, seed=41, mul=0.05).float(), randn(n, hq, d, seed=42, mul=0.2).float()
+    K[:, :, 0] = (torch.arange(L, device=DEV).float() * (log2_per_256 / 256)).repeat(n)[:, None]
+    Q[:, :, 0] = d ** 0.5 * 0.6931471805599453
+    return Q.bfloat16(), K
+
+
+@pytest.mark.parametrize("hq,hk", [(32, 8), (8, 8), (64, 8), (96, 8)])
+@pytest.mark.parametrize("size", [1e-35, 3e-37])
+def test_decode_of_steps_next_to_nothing(size, hq, hk):
+    """Steps of 2^-118 and 2^-123 beside a group of ordinary constants, more than one tile per warp, each raising the
+    maximum by less than what is let through unscaled."""
+    n, L, d = 16, 1024, 64
+    Q, K = growing_scores(n, L, hq, hk, d, 6.0)
+    V = randn(n * L, hk, d, seed=43).float() * size
+    V[:, :, :32] = 3.0
+    cache = rmm.KV4Cache.empty(n, hk, L, d)
+    rmm.kv4_store(cache, K, V, i32([0] * n), i32(cum([L] * n)))
+    assert 0 < cache.vs[..., 1, 0].float().max().item() < 2.0 ** -114
+    w_out = torch.empty(n, hk, L, device=DEV)
+    O, lse, ws = rmm.kv4_attn(Q, cache, i32([L] * n), w_out=w_out)
+    rmm.check(ws)
+    pick = [0, 7, 15]
+    sub = rmm.KV4Cache(*(t[pick].contiguous() for t in (cache.kc, cache.ks, cache.vc, cache.vs)))
+    check_decode(Q[pick], sub, [L] * 3, O[pick], lse[pick], d ** -0.5, w_out[pick])
