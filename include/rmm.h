@@ -538,8 +538,9 @@ size_t rmm_kv4_attn_workspace_size(int64_t batch, int64_t h_q, int64_t h_kv, int
  * Workspace 1 KiB-aligned, its first word the status word (rmm_check), cleared
  * at the start; RMM_STATUS_BIT_NONFINITE: a head's sum is not a positive finite
  * number. Slots at and past lens[b] are not used. Queries beyond 2^100 may
- * overflow (infinite or NaN results); a probability times step 2^-29 or more
- * below the sequence's largest loses bits of its own. */
+ * overflow (infinite or NaN results); a probability times step 2^-26 or more
+ * below its query head's largest in the sequence loses bits of its own (what it
+ * is rounded off by stays below 2^-37 of that largest product). */
 rmm_status rmm_kv4_attn(const void* Q, int64_t q_ss, int64_t q_hs, const uint8_t* kc, const void* ks,
                         const uint8_t* vc, const void* vs, const int32_t* lens, int64_t batch, int64_t h_q,
                         int64_t h_kv, int64_t d, int64_t cap, float scale, rmm_dtype in, void* O, int64_t o_ss,

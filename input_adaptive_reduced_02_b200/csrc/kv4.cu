@@ -208,10 +208,15 @@ __device__ __forceinline__ int32_t seq_len(const Kv4AttnArgs& a, int64_t b) {
 //       groups is one more product, the sums cut into three bf16 parts.
 //   Oᵀ  A = codes of 16 channels, the same f16 subnormals, B = p·step of the
 //       group in f16, transposed by movmatrix; p·min adds up in f32. A power of
-//       two per warp, raised as larger steps come (and O with it), keeps p·step
-//       below 2^15: 11 bits where bf16 would keep 8, which matters since a value
-//       is the small difference of its min and step·code (bf16: twice the error
-//       of the result). What lies 2^-29 below the largest p·step fades out.
+//       two per head keeps the largest p·step so far near 2^12, and its tile's
+//       below 2^15, lowered (and O with it) as larger ones come and raised again
+//       as the running maximum leaves them behind: 11 bits where bf16 would keep
+//       8, which matters since a value is the small difference of its min and
+//       step·code (bf16: twice the error of the result). It follows p·step, not
+//       the step, since a token of large values may have next to no weight; that
+//       costs 1 % (batch of 32 x 8192: 81.4 us, one power of two from the steps
+//       80.2). What lies 2^-26 below the head's largest p·step loses bits, and
+//       below 2^-37 fades out.
 // So a word of 8 codes costs one shift and four masks. What bounds the kernel
 // is the rate of such instructions, then HBM.
 // With up to 4 query heads per key head a tile has two halves of 16 tokens: the
@@ -273,6 +278,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ float step_of(uint32_t sm) { return __uint_as_float(sm << 16); }
+// the largest magnitude of a row's steps
+template <int NG>
+__device__ __forceinline__ float top_step(const uint32_t (&sm)[NG]) {
+  uint32_t m = sm[0] & 0x7FFFu;
+#pragma unroll
+  for (int g = 1; g < NG; ++g) m = max(m, sm[g] & 0x7FFFu);
+  return __uint_as_float(m << 16);
+}
 __device__ __forceinline__ float min_of(uint32_t sm) { return __uint_as_float(sm & 0xFFFF0000u); }
 
 // NW consecutive 32-bit words from shared memory, 4·NW-byte aligned (NW 1, 2, 4) or 4-byte (3)
@@ -527,13 +540,14 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
   }
 
   float o[NT][2 * NG][4], om[NT][NG][2], nm[NT][2], l[NT][2];
-  uint32_t v_exp = 127, step_lim = 0;  // exponent of the power of two; steps (bf16 bits) it is good for: none yet
+  float up[NT][2], lim[NT][2];  // the power of two; 4 times the largest p·step it was chosen for (0: none yet)
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       nm[n][x] = INFINITY;  // minus the maximum: none yet
-      l[n][x] = 0.f;
+      l[n][x] = lim[n][x] = 0.f;
+      up[n][x] = 1.f;
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -614,31 +628,24 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
         }
     }
     // ---- softmax: p = 2^(t·fh - maximum), the maximum one the whole warp uses
-    float pr[NT][4];
-    float top = -INFINITY;
+    uint32_t s0[NG], s1[NG];  // the values' steps and minima
+    lds_words<NG>(s0, vs + (16 * lh + r) * (4 * NG));
+    lds_words<NG>(s1, vs + (16 * lh + r + 8) * (4 * NG));
+    const float step0 = top_step<NG>(s0), step1 = top_step<NG>(s1);
+    float pr[NT][4], big[NT][4];  // p, p·up
+    float top = -INFINITY, over = 0.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        pr[n][c] = fmaf(t[n][c], fh[n][c & 1], nm[n][c & 1]);
-        top = fmaxf(top, pr[n][c]);
+      for (int x = 0; x < 2; ++x) {
+        const float y0 = fmaf(t[n][x], fh[n][x], nm[n][x]), y1 = fmaf(t[n][2 + x], fh[n][x], nm[n][x]);
+        top = max3(top, y0, y1);
+        pr[n][x] = ex2f(y0), pr[n][2 + x] = ex2f(y1);
+        big[n][x] = pr[n][x] * up[n][x], big[n][2 + x] = pr[n][2 + x] * up[n][x];
+        over = max3(over, big[n][x] * step0, big[n][2 + x] * step1);
       }
-    uint32_t top_step = 0;  // of this lane's share of the values' steps
-    constexpr int WORDS = TT * NG;
-#pragma unroll
-    for (int i = 0; i < (WORDS + 31) / 32; ++i)
-      top_step = max(top_step, reinterpret_cast<const uint32_t*>(vs)[(lane + 32 * i) % WORDS] & 0x7FFFu);
     const bool tail = TT * tile + TT > rows;
-    if (__any_sync(0xffffffffu, tail || top > kKvRescale || top_step > step_lim)) {
-      top_step = __reduce_max_sync(0xffffffffu, top_step);
-      float fv = 1.f;
-      if (top_step > step_lim) {  // the largest step becomes 2^5 to 2^6, one binade more is let through
-        // at most 2^119: p up to 2^8 times it is finite, and its reciprocal a normal number
-        const uint32_t e = top_step >> 7, next = min(max(259 - int32_t(e), 1), 246);
-        if (step_lim > 0) fv = __uint_as_float(uint32_t(max(127 + int32_t(next) - int32_t(v_exp), 0)) << 23);
-        v_exp = next;
-        step_lim = (e + 1) << 7 | 0x7Fu;
-      }
+    if (__any_sync(0xffffffffu, tail || top > kKvRescale || over > 0x1p15f)) {
       if (tail) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -657,43 +664,43 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
           const float nm2 = fminf(nm[n][x], -mx);
           const float f = nm2 == nm[n][x] ? 1.f : ex2f(nm2 - nm[n][x]);  // 0 the first time
           nm[n][x] = nm2;
+          pr[n][x] = t[n][x] == -INFINITY ? 0.f : ex2f(fmaf(t[n][x], fh[n][x], nm2));
+          pr[n][2 + x] = t[n][2 + x] == -INFINITY ? 0.f : ex2f(fmaf(t[n][2 + x], fh[n][x], nm2));
+          float ps = fmaxf(pr[n][x] * step0, pr[n][2 + x] * step1);
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) ps = fmaxf(ps, __shfl_xor_sync(0xffffffffu, ps, s));
+          // 4 times the largest p·step becomes 2^14 to 2^15. At most 2^119: p up to 2^8 times it is finite.
+          lim[n][x] = fmaxf(lim[n][x] * f, 4.f * ps);
+          const int32_t e = min(max(268 - int32_t(__float_as_uint(lim[n][x]) >> 23), 1), 246);
+          const int32_t de = e - int32_t(__float_as_uint(up[n][x]) >> 23);
+          const float fv = f * __uint_as_float(uint32_t(min(max(127 + de, 0), 254)) << 23);
+          up[n][x] = __uint_as_float(uint32_t(e) << 23);
+          big[n][x] = pr[n][x] * up[n][x], big[n][2 + x] = pr[n][2 + x] * up[n][x];
           l[n][x] *= f;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             om[n][g][x] *= f;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              o[n][2 * g + u][x] *= f * fv;
-              o[n][2 * g + u][2 + x] *= f * fv;
+              o[n][2 * g + u][x] *= fv;
+              o[n][2 * g + u][2 + x] *= fv;
             }
           }
-          pr[n][x] = t[n][x] == -INFINITY ? -INFINITY : fmaf(t[n][x], fh[n][x], nm2);
-          pr[n][2 + x] = t[n][2 + x] == -INFINITY ? -INFINITY : fmaf(t[n][2 + x], fh[n][x], nm2);
         }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) pr[n][c] = ex2f(pr[n][c]);
       l[n][0] += pr[n][0] + pr[n][2];
       l[n][1] += pr[n][1] + pr[n][3];
     }
     // ---- values
-    const float up = __uint_as_float(v_exp << 23);
-    float big[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) big[n][c] = pr[n][c] * up;
-    uint32_t wl[HALVES][NG], wh[HALVES][NG], s0[NG], s1[NG];
+    uint32_t wl[HALVES][NG], wh[HALVES][NG];
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
       const uint8_t* v0 = vc + (16 * h + 2 * j) * (16 * NG) + r * (2 * NG);
       pair_halves<NG>(wl[h], v0, v0 + 16 * NG);
       pair_halves<NG>(wh[h], v0 + 8 * (16 * NG), v0 + 9 * (16 * NG));
     }
-    lds_words<NG>(s0, vs + (16 * lh + r) * (4 * NG));
-    lds_words<NG>(s1, vs + (16 * lh + r + 8) * (4 * NG));
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const float st0 = step_of(s0[g]), mn0 = min_of(s0[g]), st1 = step_of(s1[g]), mn1 = min_of(s1[g]);
@@ -741,9 +748,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
       }
     }
   float* mine = reinterpret_cast<float*>(ring);  // [HEADS][D]
-  const float down = __uint_as_float((254u - v_exp) << 23);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int n = 0; n < NT; ++n) {
+    const float down[2] = {1.f / up[n][0], 1.f / up[n][1]};
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -751,7 +758,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, NT == 1 ? 2 : 1) kv4_attn_split
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           mine[(8 * n + 2 * j + (c & 1)) * D + 32 * g + 16 * u + 8 * (c >> 1) + r] =
-              fmaf(o[n][2 * g + u][c] * (c < 2 ? 0x1p24f : 0x1p20f), down, om[n][g][c & 1]);
+              fmaf(o[n][2 * g + u][c] * (c < 2 ? 0x1p24f : 0x1p20f), down[c & 1], om[n][g][c & 1]);
+  }
   __syncthreads();
   if (tid < heads) {  // m_sh becomes the warps' factors (a head's second column: of the second half)
     float m = m_sh[0][tid];  // the first warp has a tile

@@ -1,13 +1,17 @@
 """The attention operators where a value, a size or a neighbour is unusual: rows
-that a tile leaves idle, steps next to nothing. Tolerances as derived in test_gpu_attention.py unless a
-test derives its own."""
+that a tile leaves idle, steps next to nothing, values of very different size in
+one sequence. Tolerances as derived in test_gpu_attention.py unless a test
+derives its own."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 from input_adaptive_reduced_02_b200 import rmm
-from test_gpu_attention import DEV, check_decode, check_prompt, cum, i32, make_prompt, randn
+from oracle import attention_oracle as AO
+from test_gpu_attention import (DECODES, DEV, check_decode, check_prompt, cum, f64, filled_cache, i32, make_prompt, randn,
+                                score_error, stored)
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +82,61 @@ def test_decode_of_steps_next_to_nothing(size, hq, hk):
     pick = [0, 7, 15]
     sub = rmm.KV4Cache(*(t[pick].contiguous() for t in (cache.kc, cache.ks, cache.vc, cache.vs)))
     check_decode(Q[pick], sub, [L] * 3, O[pick], lse[pick], d ** -0.5, w_out[pick])
+
+
+def check_decode_f16(Q, cache, lens, O, lse, scale):
+    """Outputs of dtype f32, by the header's arithmetic. p·step is rounded to f16: off by at most 2^-11 of itself, or,
+    next to nothing, by half of the least f16 subnormal, 2^-25 under a power of two that keeps 4 times the head's
+    largest p·step at 2^14 at least, so 2^-37 of that largest product; times codes up to 15. p·minimum and all
+    sums stay in f32 (2^-18). Scores move numerator and denominator by 2.2·E."""
+    n, hq, d = Q.shape
+    gq = hq // cache.heads
+    assert O.dtype == torch.float32
+    for b in range(n):
+        for h in range(cache.heads):
+            k, v, (kc, ks, vc, vs) = stored(cache, b, h, lens[b])
+            steps = AO.dequantise(vc, vs[..., 0], 0 * vs[..., 1])
+            vmag = AO.dequantise(vc, vs[..., 0], np.abs(vs[..., 1]))
+            kmag = np.maximum(np.abs(k), AO.dequantise(kc, ks[..., 0], np.abs(ks[..., 1])))
+            q = f64(Q[b, h * gq:(h + 1) * gq])
+            Or, lr, P, _ = AO.attention(q, k, v, scale, False)
+            E = score_error(np.max(scale * np.abs(q) @ kmag.T, axis=1), d)
+            largest = (P * vs[..., 0].max(1)).max(1)
+            tol = 2.0 ** -11 * (P @ steps) + (2.2 * E[:, None] + 2.0 ** -18) * (P @ vmag)
+            tol += (len(k) * 15 * 2.0 ** -37 * largest)[:, None]
+            err = np.abs(f64(O[b, h * gq:(h + 1) * gq]) - Or)
+            assert np.all(err <= tol), f"worst {np.max(err / tol):.2f}"
+            gl = f64(lse[b, h * gq:(h + 1) * gq])
+            assert np.all(np.abs(gl - lr) <= E + 2.0 ** -21 * (1 + np.abs(lr)))
+
+
+@pytest.mark.parametrize("case", [c for c in DECODES if 0 not in c[0]],
+                         ids=lambda c: f"l{'-'.join(map(str, c[0]))}_h{c[2]}-{c[3]}_d{c[4]}")
+def test_decode_keeps_f16_of_the_probabilities_times_steps(case):
+    lens, cap, hq, hk, d = case
+    cache = filled_cache(lens, cap, hk, d, seed=7 * d + cap)
+    Q = randn(len(lens), hq, d, seed=19, mul=2.0)
+    O, lse, ws = rmm.kv4_attn(Q, cache, i32(lens))
+    rmm.check(ws)
+    check_decode_f16(Q, cache, lens, O, lse, d ** -0.5)
+
+
+@pytest.mark.parametrize("at", [0, 5, 700], ids=lambda x: f"token{x}")
+@pytest.mark.parametrize("ratio,below", [(24, 40), (31, 40), (60, 70), (100, 60)])
+@pytest.mark.parametrize("hq,hk", [(8, 2), (16, 2), (24, 2)])
+def test_decode_of_an_outlier_that_hardly_counts(hq, hk, ratio, below, at):
+    """One token's values are 2^ratio times the others', its probability about 2^-below of theirs: where the others' p·step
+    are the larger ones they keep their bits, and where its own is, it does."""
+    L, d = 1000, 64
+    K, V = randn(L, hk, d, seed=51, mul=0.05).float(), randn(L, hk, d, seed=52).float()
+    Q = randn(1, hq, d, seed=53, mul=0.2).float()
+    Q[:, :, 0] = d ** 0.5 * 0.6931471805599453
+    K[:, :, 0] = 0.0
+    K[at, :, 0] = -below
+    V[at] *= 2.0 ** ratio
+    Q = Q.bfloat16()
+    cache = rmm.KV4Cache.empty(1, hk, L, d)
+    rmm.kv4_store(cache, K, V, i32([0]), i32([0, L]))
+    O, lse, ws = rmm.kv4_attn(Q, cache, i32([L]))
+    rmm.check(ws)
+    check_decode_f16(Q, cache, [L], O, lse, d ** -0.5)
