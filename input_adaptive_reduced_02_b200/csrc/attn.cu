@@ -776,7 +776,8 @@ attn_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
           }
           tc_fence_after();
           // pairs [lo, hi) of this half of the tile count: queries that see this key, and that exist
-          const int32_t lo = a.causal ? (k - off - i * p.nq_tile) * p.g - 64 * half : 0;
+          // (cut at 0 first: a key long before the queries lies 2^31 pairs before them)
+          const int32_t lo = a.causal ? max(k - off - i * p.nq_tile, 0) * p.g - 64 * half : 0;
           const int32_t hi = min(p.nq_tile, S_q - i * p.nq_tile) * p.g - 64 * half;
           const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < 64;
           const float* nl = lse_sh + ring * kRows + 64 * half;

@@ -1,7 +1,7 @@
 """The attention operators where a value, a size or a neighbour is unusual: rows
 that a tile leaves idle, steps next to nothing, values of very different size in
-one sequence. Tolerances as derived in test_gpu_attention.py unless a test
-derives its own."""
+one sequence, more (key, head) pairs than 31 bits hold. Tolerances as derived in
+test_gpu_attention.py unless a test derives its own."""
 from __future__ import annotations
 
 import numpy as np
@@ -140,3 +140,25 @@ def test_decode_of_an_outlier_that_hardly_counts(hq, hk, ratio, below, at):
     O, lse, ws = rmm.kv4_attn(Q, cache, i32([L]))
     rmm.check(ws)
     check_decode_f16(Q, cache, [L], O, lse, d ** -0.5)
+
+
+# ---------------------------------------------------------------- long contexts
+def test_key_weights_of_keys_2_to_31_pairs_before_the_queries():
+    """Three new tokens of 128 query heads on one key head after 2^24 + 197 earlier ones: the first keys lie more than 2^31
+    (query, head) pairs before the first query."""
+    S_q, S_k, hq, d = 3, (1 << 24) + 200, 128, 8
+    Q, K, V = randn(S_q, hq, d, seed=61), randn(S_k, 1, d, seed=62), randn(S_k, 1, d, seed=63)
+    st = rmm.status_word()
+    _, lse = rmm.attn_prompt(Q, K, V, status=st)
+    w = rmm.attn_key_weights(Q, K, lse, status=st)
+    rmm.check(st)
+    scale = d ** -0.5
+    q = Q.double().reshape(S_q * hq, d)
+    for k0, k1 in ((0, 1000), (S_k // 2, S_k // 2 + 1000), (S_k - 1000, S_k)):
+        x = scale * (q @ K[k0:k1, 0].double().T).reshape(S_q, hq, k1 - k0)
+        seen = torch.arange(k0, k1, device=DEV) <= torch.arange(S_q, device=DEV)[:, None] + S_k - S_q
+        ref = (torch.exp(x - lse.T.double()[:, :, None]) * seen[:, None]).sum((0, 1))
+        E = score_error((scale * q.abs() @ K[k0:k1, 0].double().abs().T).max().item(), d)
+        assert ((w[0, k0:k1] - ref).abs() <= (2.1 * E + 2.0 ** -18) * ref).all()
+    # every row's probabilities add up to 1: a row's lse is off by E + 2^-21·(1 + |lse|) at most, |lse| < 32
+    assert abs(w.double().sum().item() - S_q * hq) <= S_q * hq * 2.0 ** -14
