@@ -515,8 +515,9 @@ rmm_status rmm_attn_key_weights(const void* Q, int64_t q_ts, int64_t q_hs, const
  * sequence (T == n_seq). K, V [T][h_kv][d] of dtype in (bf16 or f32; any
  * strides). w (nullable, [n_seq][h_kv][cap] f32): the slots' running weights,
  * set to w_new[h][t] (f32 [h_kv][T]) or, w_new NULL, to 0. Tokens whose slot
- * is outside [0, cap) are left out and set RMM_STATUS_BIT_RANGE; a NaN or Inf
- * sets RMM_STATUS_BIT_NONFINITE (its group's contents are then unspecified).
+ * is outside [0, cap) are left out and set RMM_STATUS_BIT_RANGE; a NaN or Inf,
+ * or a group whose max - min overflows f32 or whose minimum overflows bf16, sets
+ * RMM_STATUS_BIT_NONFINITE (its contents are then unspecified).
  * Slots must not repeat within a call. */
 rmm_status rmm_kv4_store(const void* K, int64_t k_ts, int64_t k_hs, const void* V, int64_t v_ts, int64_t v_hs,
                          rmm_dtype in, const int32_t* cu, const int32_t* start, int64_t n_seq, int64_t T, int64_t h_kv,

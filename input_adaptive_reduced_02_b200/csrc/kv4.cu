@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
   bool odd = false;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    float2 p[4], zero = make_float2(0.f, 0.f);  // zero: NaN where an element is NaN or infinite
+    float2 p[4], zero = make_float2(0.f, 0.f);  // zero: NaN where an element, the step or the minimum is not finite
     float lo = x[kv][0], hi = lo;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -136,7 +136,6 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
       hi = max3(hi, p[e].x, p[e].y);
       zero = fma2(p[e], make_float2(0.f, 0.f), zero);
     }
-    odd |= zero.x + zero.y != 0.f;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -144,7 +143,10 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_store_kernel(const Kv4Store
     }
     // (step, minimum) as stored; the IEEE quotient, so that it depends on nothing but the values
     const uint32_t sm = pack_bf16x2(fifteenth(hi - lo), lo);
-    const uint32_t codes = codes_of(p, __uint_as_float(sm << 16), __uint_as_float(sm & 0xFFFF0000u));
+    const float step = __uint_as_float(sm << 16), mn = __uint_as_float(sm & 0xFFFF0000u);
+    zero = fma2(make_float2(step, mn), make_float2(0.f, 0.f), zero);
+    odd |= zero.x + zero.y != 0.f;
+    const uint32_t codes = codes_of(p, step, mn);
     // the values' half-words need one nibble from each of the group's four lanes
     uint32_t half[2] = {0u, 0u};  // half-words r = 2j, 2j + 1 of group w
     if (kv == 1) {

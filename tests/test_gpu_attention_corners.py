@@ -1,7 +1,7 @@
 """The attention operators where a value, a size or a neighbour is unusual: rows
 that a tile leaves idle, steps next to nothing, values of very different size in
-one sequence, more (key, head) pairs than 31 bits hold. Tolerances as derived in
-test_gpu_attention.py unless a test derives its own."""
+one sequence, more (key, head) pairs than 31 bits hold, groups that overflow.
+Tolerances as derived in test_gpu_attention.py unless a test derives its own."""
 from __future__ import annotations
 
 import numpy as np
@@ -162,3 +162,25 @@ def test_key_weights_of_keys_2_to_31_pairs_before_the_queries():
         assert ((w[0, k0:k1] - ref).abs() <= (2.1 * E + 2.0 ** -18) * ref).all()
     # every row's probabilities add up to 1: a row's lse is off by E + 2^-21·(1 + |lse|) at most, |lse| < 32
     assert abs(w.double().sum().item() - S_q * hq) <= S_q * hq * 2.0 ** -14
+
+
+# ---------------------------------------------------------------- store
+@pytest.mark.parametrize("plane", [0, 1], ids=["keys", "values"])
+@pytest.mark.parametrize("lo,hi,fits", [(-3e38, 3e38, False), (-2e38, 1e38, True), (-3.4e38, -3.39e38, False),
+                                        (3.3895e38, 3.3895e38, True), (3.4e38, 3.4e38, False)])
+def test_store_reports_steps_and_minima_that_overflow(lo, hi, fits, plane):
+    """Finite values whose group's max - min overflows f32, or whose minimum overflows bf16 (largest 3.3895e38)."""
+    kv = [randn(3, 2, 64, seed=s).float() for s in (71, 72)]
+    kv[plane][1, 1, 32:] = torch.linspace(lo, hi, 32, dtype=torch.float64).float().to(DEV)
+    kv[plane][1, 1, 32], kv[plane][1, 1, 63] = lo, hi
+    assert torch.isfinite(kv[plane]).all()
+    cache = rmm.KV4Cache.empty(1, 2, 3, 64)
+    st = rmm.status_word()
+    rmm.kv4_store(cache, *kv, i32([0]), i32([0, 3]), status=st)
+    if fits:
+        rmm.check(st)
+        assert torch.isfinite(cache.ks).all() and torch.isfinite(cache.vs).all()
+        return
+    with pytest.raises(rmm.RMMError) as e:
+        rmm.check(st)
+    assert e.value.status == rmm.RMM_ERR_NONFINITE
