@@ -524,7 +524,7 @@ rmm_status rmm_kv4_store(const void* K, int64_t k_ts, int64_t k_hs, const void* 
                          int64_t d, int64_t cap, uint8_t* kc, void* ks, uint8_t* vc, void* vs, const float* w_new,
                          float* w, uint32_t* status_word, cudaStream_t stream);
 
-/* Bytes of workspace rmm_kv4_attn needs (weights: w_out is given). */
+/* Bytes of workspace rmm_kv4_attn needs (weights: w_out is given); 0 for sizes it refuses. */
 size_t rmm_kv4_attn_workspace_size(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, int weights);
 
 /* One decode step: O[b] = softmax(scale·q·Kᵀ)·V over the first lens[b] cached
@@ -559,6 +559,7 @@ typedef struct {
   int64_t row_bytes;
 } rmm_cache_plane;
 
+/* Bytes of workspace rmm_cache_evict needs; 0 for sizes it refuses. */
 size_t rmm_cache_evict_workspace_size(int64_t batch, int64_t heads, int64_t budget);
 
 /* Keep at most `budget` of each (sequence, head)'s lens[b] cached tokens: the

@@ -61,6 +61,10 @@ rmm_status check_prompt(const AttnArgs& a, rmm_dtype in) {
   if ((r = check_heads(a.h_q, a.h_kv, 128))) return r;
   if (a.d < 1) return fail(RMM_ERR_INVALID, "d must be at least 1");
   if (a.d % 8 != 0 || a.d > 128) return fail(RMM_ERR_UNSUPPORTED, "d must be a multiple of 8, at most 128");
+  // one block per tile (256 rows of queries, or 256 keys) and key head
+  const int64_t span = 2 * (128 / (a.h_q / a.h_kv));
+  if (std::max(a.T_q / span, a.T_k / 256) + a.n_seq + 1 > kMaxI32 / a.h_kv)
+    return fail(RMM_ERR_UNSUPPORTED, "more tiles of all sequences and heads than a grid holds");
   if ((r = check_scale(a.scale))) return r;
   if (a.n_seq != 1 && (!a.cu_q || !a.cu_k))
     return fail(RMM_ERR_INVALID, "cu_q and cu_k may be NULL for a single sequence only");
@@ -76,7 +80,7 @@ rmm_status check_planes(const Kv4Planes& c, int64_t batch, int64_t h_kv, int64_t
   if (batch > 0 && (!c.kc || !c.ks || !c.vc || !c.vs)) return fail(RMM_ERR_INVALID, "a cache plane is NULL");
   if (!aligned(c.kc, 16) || !aligned(c.ks, 16) || !aligned(c.vc, 16) || !aligned(c.vs, 16))
     return fail(RMM_ERR_INVALID, "the cache planes must be 16-byte aligned");
-  if (batch * h_kv > 65535) return fail(RMM_ERR_UNSUPPORTED, "more than 65535 (sequence, head) pairs");
+  if (batch > 65535 || h_kv > 65535 || batch * h_kv > 65535) return fail(RMM_ERR_UNSUPPORTED, "more than 65535 (sequence, head) pairs");
   return RMM_OK;
 }
 
@@ -212,6 +216,7 @@ rmm_status rmm_kv4_store(const void* K, int64_t k_ts, int64_t k_hs, const void* 
 
 size_t rmm_kv4_attn_workspace_size(int64_t batch, int64_t h_q, int64_t h_kv, int64_t d, int64_t cap, int weights) {
   if (batch < 0 || h_q < 1 || h_kv < 1 || d < 1 || cap < 1) return 0;
+  if (batch > 65535 || h_q > 65535 || h_kv > 65535 || d > kKv4MaxD || cap > kMaxSelectK) return 0;  // refused
   return kv4_ws(batch, h_q, h_kv, d, cap, weights != 0).bytes;
 }
 
@@ -273,6 +278,7 @@ rmm_status rmm_kv4_attn(const void* Q, int64_t q_ss, int64_t q_hs, const uint8_t
 
 size_t rmm_cache_evict_workspace_size(int64_t batch, int64_t heads, int64_t budget) {
   if (batch < 0 || heads < 1 || budget < 1) return 0;
+  if (batch > kMaxI32 || heads > kMaxI32 || batch * heads > kMaxI32 || budget > kMaxSelectK) return 0;  // refused
   return size_t(1024 + up1k(batch * heads * 4) + up1k(batch * heads * budget * 4));
 }
 
@@ -283,7 +289,8 @@ rmm_status rmm_cache_evict(const float* w, const int32_t* lens, int64_t batch, i
   if (batch < 0) return fail(RMM_ERR_INVALID, "negative size");
   if (heads < 1 || cap < 1) return fail(RMM_ERR_INVALID, "heads and cap must be at least 1");
   if (cap > kMaxSelectK) return fail(RMM_ERR_UNSUPPORTED, "cap above 2^21");
-  if (batch * heads > kMaxI32) return fail(RMM_ERR_UNSUPPORTED, "too many (sequence, head) pairs");
+  if (batch > kMaxI32 || heads > kMaxI32 || batch * heads > kMaxI32)
+    return fail(RMM_ERR_UNSUPPORTED, "too many (sequence, head) pairs");
   if (budget < 1 || budget > cap_out) return fail(RMM_ERR_INVALID, "budget must be in [1, cap_out]");
   if (cap_out > kMaxSelectK) return fail(RMM_ERR_UNSUPPORTED, "cap_out above 2^21");
   if (sink < 0 || recent < 0 || sink + recent > budget)

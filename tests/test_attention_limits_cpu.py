@@ -1,0 +1,37 @@
+"""Sizes of the attention operators at which a count would not fit its integer:
+refused on the host (no GPU)."""
+from __future__ import annotations
+
+import pytest
+
+from input_adaptive_reduced_02_b200 import rmm
+from test_attention_abi_cpu import DECODE, EVICT, P, PROMPT, STORE, UNSUPPORTED, WEIGHTS, call
+
+WIDE = dict(d=8, q_ts=65535 * 8, q_hs=8, k_ts=65535 * 8, k_hs=8, h_q=65535, h_kv=65535, n_seq=65535)
+
+
+@pytest.mark.parametrize("name,base,changes", [
+    # blocks of every sequence and head: 2^32 - 131071, and just above 2^32, where the count would wrap round
+    ("rmm_attn_prompt", PROMPT, dict(WIDE, v_ts=65535 * 8, v_hs=8, o_ts=65535 * 8, o_hs=8)),
+    ("rmm_attn_prompt", PROMPT, dict(WIDE, v_ts=65535 * 8, v_hs=8, o_ts=65535 * 8, o_hs=8, T_q=1024)),
+    ("rmm_attn_key_weights", WEIGHTS, WIDE), ("rmm_attn_key_weights", WEIGHTS, dict(WIDE, T_k=1024)),
+    # products of two sizes that are 0 modulo 2^64
+    ("rmm_kv4_store", STORE, dict(n_seq=1 << 32, h_kv=1 << 32)),
+    ("rmm_kv4_attn", DECODE, dict(batch=1 << 62)),
+    ("rmm_cache_evict", EVICT, dict(batch=1 << 32, heads=1 << 32)),
+], ids=lambda x: x if isinstance(x, str) else "")
+def test_counts_that_do_not_fit_are_refused(name, base, changes):
+    got, text = call(name, base, changes)
+    assert got == UNSUPPORTED, (got, text)
+
+
+def test_workspace_sizes_of_refused_calls_are_zero():
+    size = rmm.lib().rmm_kv4_attn_workspace_size
+    assert size(65535, 8, 1, 64, 1 << 21, 1) > 0
+    for bad in ((1 << 62, 8, 1, 64, 16), (1, 1 << 40, 1, 64, 16), (1, 8, 1 << 40, 64, 16), (1, 8, 1, 160, 16),
+                (1, 8, 1, 64, (1 << 21) + 1)):
+        assert size(*bad, 1) == 0
+    size = rmm.lib().rmm_cache_evict_workspace_size
+    assert size(65535, 8, 1 << 21) > 0
+    for bad in ((1 << 32, 1 << 32, 16), (1, 1 << 62, 16), (1, 1, (1 << 21) + 1)):
+        assert size(*bad) == 0
