@@ -154,6 +154,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _status_ptr(status: torch.Tensor | None, device):
+    """The address of a status word (status_word()) on the call's device."""
+    if status is None:
+        return None
+    if status.dtype not in (torch.int32, torch.uint32) or status.numel() < 1 or status.device != device:
+        raise ValueError(f"status must be a 32-bit integer tensor on {device} (status_word())")
+    return status.data_ptr()
+
+
 def _mat(t: torch.Tensor, name: str):
     """(batch, rows, cols, ld, batch_stride) of a 2-D or 3-D CUDA tensor."""
     if not t.is_cuda:
@@ -200,6 +209,7 @@ class Workspace:
     def __init__(self, nbytes: int, device):
         self.nbytes = int(nbytes)
         self._buf = torch.empty(self.nbytes + 1024, dtype=torch.uint8, device=device)
+        self.device = self._buf.device
         base = self._buf.data_ptr()
         self.offset = (-base) % 1024
         self.ptr = base + self.offset
@@ -210,6 +220,8 @@ class Workspace:
 
 
 def _ensure_ws(ws, nbytes, device):
+    if ws is not None and ws.device != device:
+        raise ValueError(f"the workspace is on {ws.device}, the call on {device}")
     if ws is None or ws.nbytes < nbytes:
         return Workspace(nbytes, device)
     return ws
@@ -705,7 +717,7 @@ def attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.T
     status_code = lib().rmm_attn_prompt(
         Q.data_ptr(), q_ts, q_hs, K.data_ptr(), k_ts, k_hs, V.data_ptr(), v_ts, v_hs, _ptr(cu_q), _ptr(cu_k), n, T_q, T_k,
         h_q, h_kv, d, d ** -0.5 if scale is None else scale, causal, _dtype(Q), out.data_ptr(), o_ts, o_hs,
-        _out_code(out.dtype), lse.data_ptr(), _ptr(status), _stream(Q))
+        _out_code(out.dtype), lse.data_ptr(), _status_ptr(status, device), _stream(Q))
     if status_code:
         _check(status_code)
     return out, lse
@@ -726,7 +738,8 @@ def attn_key_weights(Q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, cu_q: 
     _f32_shape(out, "out", (h_kv, T_k), Q.device)
     _check(lib().rmm_attn_key_weights(_ptr(Q), q_ts, q_hs, _ptr(K), k_ts, k_hs, _ptr(cu_q), _ptr(cu_k), n, T_q, T_k,
                                       h_q, h_kv, d, float(d ** -0.5 if scale is None else scale), int(causal),
-                                      _dtype(Q), _ptr(lse), _ptr(w_in), _ptr(out), _ptr(status), _stream(Q)))
+                                      _dtype(Q), _ptr(lse), _ptr(w_in), _ptr(out), _status_ptr(status, Q.device),
+                                      _stream(Q)))
     return out
 
 
@@ -794,7 +807,7 @@ def kv4_store(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, start: torch.Te
     status_code = lib().rmm_kv4_store(
         K.data_ptr(), k_ts, k_hs, V.data_ptr(), v_ts, v_hs, _dtype(K), _ptr(cu), start.data_ptr(), batch, T, h, d,
         cache.cap, kc.data_ptr(), cache.ks.data_ptr(), cache.vc.data_ptr(), cache.vs.data_ptr(), _ptr(w_new),
-        _ptr(cache.w), _ptr(status), _stream(K))
+        _ptr(cache.w), _status_ptr(status, device), _stream(K))
     if status_code:
         _check(status_code)
     return cache

@@ -1,8 +1,9 @@
 """Sizes of the attention operators at which a count would not fit its integer:
-refused on the host (no GPU)."""
+refused on the host, as are buffers of another device (no GPU)."""
 from __future__ import annotations
 
 import pytest
+import torch
 
 from input_adaptive_reduced_02_b200 import rmm
 from test_attention_abi_cpu import DECODE, EVICT, P, PROMPT, STORE, UNSUPPORTED, WEIGHTS, call
@@ -35,3 +36,19 @@ def test_workspace_sizes_of_refused_calls_are_zero():
     assert size(65535, 8, 1 << 21) > 0
     for bad in ((1 << 32, 1 << 32, 16), (1, 1 << 62, 16), (1, 1, (1 << 21) + 1)):
         assert size(*bad) == 0
+
+
+def test_status_words_and_workspaces_of_another_device_are_refused():
+    """Their addresses would be written to by kernels of the call's device."""
+    there, here = torch.device("cuda", 0), torch.device("cpu")
+    assert rmm._status_ptr(None, there) is None
+    word = rmm.status_word("cpu")
+    assert rmm._status_ptr(word, here) == word.data_ptr()
+    for bad, device in ((word, there), (torch.zeros(1, dtype=torch.int64), here), (torch.zeros(1), here),
+                        (torch.zeros(0, dtype=torch.int32), here)):
+        with pytest.raises(ValueError, match="status must be"):
+            rmm._status_ptr(bad, device)
+    ws = rmm.Workspace(64, "cpu")
+    assert rmm._ensure_ws(ws, 64, here) is ws and rmm._ensure_ws(ws, 65, here) is not ws
+    with pytest.raises(ValueError, match="workspace is on"):
+        rmm._ensure_ws(ws, 64, there)

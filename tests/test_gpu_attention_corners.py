@@ -184,3 +184,17 @@ def test_store_reports_steps_and_minima_that_overflow(lo, hi, fits, plane):
     with pytest.raises(rmm.RMMError) as e:
         rmm.check(st)
     assert e.value.status == rmm.RMM_ERR_NONFINITE
+
+
+# ---------------------------------------------------------------- refusals of the binding
+def test_status_words_that_kernels_cannot_write_are_refused():
+    q, k = randn(4, 2, 64), randn(4, 1, 64)
+    lse = torch.zeros(2, 4, device=DEV)
+    cache = rmm.KV4Cache.empty(1, 1, 8, 64)
+    for bad in (rmm.status_word("cpu"), torch.zeros(1, dtype=torch.int64, device=DEV), torch.zeros(1, device=DEV)):
+        for call in (lambda: rmm.attn_prompt(q, k, k, status=bad), lambda: rmm.attn_key_weights(q, k, lse, status=bad),
+                     lambda: rmm.kv4_store(cache, k, k, i32([0]), i32([0, 4]), status=bad)):
+            with pytest.raises(ValueError, match="status must be"):
+                call()
+    with pytest.raises(ValueError, match="workspace is on"):
+        rmm.kv4_attn(q[:1], cache, i32([0]), workspace=rmm.Workspace(1 << 20, "cpu"))
