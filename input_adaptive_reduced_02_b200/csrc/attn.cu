@@ -394,7 +394,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         uint32_t s[4][32];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld_32x32b_x32(tS + 32 * x, s[x]);
-        tmem_ld_wait();
+        tmem_ld_wait(s[0]);
+#pragma unroll
+        for (int x = 1; x < 4; ++x) tmem_ld_waited(s[x]);
         const int32_t left = lim - j * kRows;  // visible keys of this tile
         if (__any_sync(0xffffffffu, left < kRows)) {
 #pragma unroll

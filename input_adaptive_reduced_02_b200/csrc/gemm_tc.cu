@@ -392,7 +392,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const uint32_t col_base = uint32_t(c_begin * cols_per_chunk);
 #pragma unroll
         for (int l = 0; l < NLD; ++l) tmem_ld_32x32b_x32(t_row + col_base + 32 * l, r[l]);
-        tmem_ld_wait();
+        tmem_ld_wait(r[0]);
+#pragma unroll
+        for (int l = 1; l < NLD; ++l) tmem_ld_waited(r[l]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -424,7 +426,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             uint32_t r0[32], r1[32];
             tmem_ld_32x32b_x32(t_row + c * 64, r0);
             tmem_ld_32x32b_x32(t_row + c * 64 + 32, r1);
-            tmem_ld_wait();
+            tmem_ld_wait(r0);
+            tmem_ld_waited(r1);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               packed[j] = pack_bf16x2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
@@ -432,7 +435,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
           } else {
             tmem_ld_32x32b_x32(t_row + c * 32, packed);
-            tmem_ld_wait();
+            tmem_ld_wait(packed);
           }
           if (c == c_end - 1) {
             // this warp's part of the accumulator read: hand it back to the leader's MMA lane
