@@ -234,7 +234,8 @@ def status_word(device="cuda") -> torch.Tensor:
 
 def check(status, stream_tensor: torch.Tensor | None = None):
     """Read and clear a device status word (a tensor from status_word(), or a
-    Workspace); raise RMMError on NaN/Inf scores or a pipeline timeout."""
+    Workspace); raise RMMError on NaN/Inf scores, a pipeline timeout or a token
+    outside its cache."""
     if isinstance(status, Workspace):
         ptr, dev = status.ptr, status._buf.device
     else:
@@ -749,11 +750,13 @@ KV4_GROUP = 32
 class KV4Cache:
     """The planes of a cache of keys and values in 4 bits (include/rmm.h has the
     layout): kc, vc [batch][heads][cap][d/2] uint8 codes, ks, vs
-    [batch][heads][cap][d/32][2] bf16 steps and minima, and optionally w
-    [batch][heads][cap] f32, the tokens' running attention weights."""
+    [batch][heads][cap][d/32][2] bf16 steps and minima, optionally w
+    [batch][heads][cap] f32, the tokens' running attention weights, and
+    optionally a status word that stores into the cache report to (empty() makes
+    both)."""
 
     def __init__(self, kc: torch.Tensor, ks: torch.Tensor, vc: torch.Tensor, vs: torch.Tensor,
-                 w: torch.Tensor | None = None):
+                 w: torch.Tensor | None = None, status: torch.Tensor | None = None):
         codes, device = kc.shape, kc.device
         if len(codes) != 4 or kc.dtype != torch.uint8 or not kc.is_cuda:
             raise ValueError("kc must be a [batch][heads][cap][d/2] uint8 CUDA tensor")
@@ -768,6 +771,8 @@ class KV4Cache:
                              f"{list(scales)} tensors on {device}")
         self.kc, self.ks, self.vc, self.vs = kc, ks, vc, vs
         self.w = None if w is None else _f32_shape(w, "w", (self.batch, self.heads, self.cap), device)
+        _status_ptr(status, device)
+        self.status = status
 
     @classmethod
     def empty(cls, batch: int, heads: int, cap: int, d: int, device="cuda", weights: bool = True) -> "KV4Cache":
@@ -778,7 +783,7 @@ class KV4Cache:
         scales = lambda: torch.zeros(batch, heads, cap, d // KV4_GROUP, 2, dtype=torch.bfloat16,  # noqa: E731
                                      device=device)
         w = torch.zeros(batch, heads, cap, dtype=torch.float32, device=device) if weights else None
-        return cls(codes(), scales(), codes(), scales(), w)
+        return cls(codes(), scales(), codes(), scales(), w, status_word(device))
 
     def planes(self):
         """The tensors whose rows belong to a token, for cache_evict."""
@@ -791,7 +796,12 @@ def kv4_store(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, start: torch.Te
     """Quantise tokens into the cache: K, V [T][heads][d] (bf16 or f32), sequence
     b's tokens [cu[b], cu[b+1]) going to its slots start[b], start[b] + 1, ...
     (cu None: one token per sequence). The slots' running weights are set to
-    w_new [heads][T], or to 0."""
+    w_new [heads][T], or to 0.
+
+    A token whose slot lies outside the cache's capacity is left out, and a
+    NaN, Inf or overflowing group is stored as it may be; both are reported in
+    `status` (None: the cache's own word) and raise at the next
+    check(cache.status), which waits for the stream."""
     T, h, d, k_ts, k_hs = _tokens(K, "K")
     tv, hv, dv, v_ts, v_hs = _tokens(V, "V")
     if tv != T or hv != h or dv != d or h != cache.heads or d != cache.d or V.dtype != K.dtype:
@@ -807,7 +817,7 @@ def kv4_store(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, start: torch.Te
     status_code = lib().rmm_kv4_store(
         K.data_ptr(), k_ts, k_hs, V.data_ptr(), v_ts, v_hs, _dtype(K), _ptr(cu), start.data_ptr(), batch, T, h, d,
         cache.cap, kc.data_ptr(), cache.ks.data_ptr(), cache.vc.data_ptr(), cache.vs.data_ptr(), _ptr(w_new),
-        _ptr(cache.w), _status_ptr(status, device), _stream(K))
+        _ptr(cache.w), _status_ptr(cache.status if status is None else status, device), _stream(K))
     if status_code:
         _check(status_code)
     return cache

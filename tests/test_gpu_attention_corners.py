@@ -198,3 +198,26 @@ def test_status_words_that_kernels_cannot_write_are_refused():
                 call()
     with pytest.raises(ValueError, match="workspace is on"):
         rmm.kv4_attn(q[:1], cache, i32([0]), workspace=rmm.Workspace(1 << 20, "cpu"))
+
+
+def test_a_full_cache_reports_the_token_it_has_no_room_for():
+    """Through the cache's own status word, without one from the caller."""
+    cache = rmm.KV4Cache.empty(2, 1, 4, 64)
+    lens, step = i32([3, 1]), randn(2, 1, 64)
+    rmm.kv4_store(cache, step, step, lens)
+    rmm.check(cache.status)
+    rmm.kv4_store(cache, step, step, lens + 1)  # slot 4 of sequence 0
+    assert (cache.ks[1, :, 2] != 0).any()
+    with pytest.raises(rmm.RMMError) as e:
+        rmm.check(cache.status)
+    assert e.value.status == rmm.RMM_ERR_INVALID
+    rmm.check(cache.status)  # reported once
+    mine = rmm.status_word()
+    rmm.kv4_store(cache, step, step, lens + 1, status=mine)
+    rmm.check(cache.status)
+    with pytest.raises(rmm.RMMError):
+        rmm.check(mine)
+    planes = (cache.kc, cache.ks, cache.vc, cache.vs, cache.w)
+    assert rmm.KV4Cache(*planes).status is None and rmm.KV4Cache(*planes, status=mine).status is mine
+    with pytest.raises(ValueError, match="status must be"):
+        rmm.KV4Cache(*planes, status=rmm.status_word("cpu"))
