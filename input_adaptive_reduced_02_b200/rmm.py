@@ -717,7 +717,7 @@ def attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.T
         _f32_shape(lse, "lse", (h_q, T_q), device)
     status_code = lib().rmm_attn_prompt(
         Q.data_ptr(), q_ts, q_hs, K.data_ptr(), k_ts, k_hs, V.data_ptr(), v_ts, v_hs, _ptr(cu_q), _ptr(cu_k), n, T_q, T_k,
-        h_q, h_kv, d, d ** -0.5 if scale is None else scale, causal, _dtype(Q), out.data_ptr(), o_ts, o_hs,
+        h_q, h_kv, d, d ** -0.5 if scale is None else float(scale), int(causal), _dtype(Q), out.data_ptr(), o_ts, o_hs,
         _out_code(out.dtype), lse.data_ptr(), _status_ptr(status, device), _stream(Q))
     if status_code:
         _check(status_code)
@@ -859,8 +859,8 @@ def kv4_attn(Q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, scale: float 
         _f32_shape(lse, "lse", (n, h_q), device)
     status_code = lib().rmm_kv4_attn(
         Q.data_ptr(), q_ss, q_hs, kc.data_ptr(), cache.ks.data_ptr(), cache.vc.data_ptr(), cache.vs.data_ptr(),
-        lens.data_ptr(), n, h_q, heads, d, cap, d ** -0.5 if scale is None else scale, _dtype(Q), out.data_ptr(), o_ss,
-        o_hs, _out_code(out.dtype), lse.data_ptr(), _ptr(w_in), _ptr(w_out), ws.ptr, ws.nbytes, _stream(Q))
+        lens.data_ptr(), n, h_q, heads, d, cap, d ** -0.5 if scale is None else float(scale), _dtype(Q), out.data_ptr(),
+        o_ss, o_hs, _out_code(out.dtype), lse.data_ptr(), _ptr(w_in), _ptr(w_out), ws.ptr, ws.nbytes, _stream(Q))
     if status_code:
         _check(status_code)
     return out, lse, ws

@@ -221,3 +221,45 @@ def test_a_full_cache_reports_the_token_it_has_no_room_for():
     assert rmm.KV4Cache(*planes).status is None and rmm.KV4Cache(*planes, status=mine).status is mine
     with pytest.raises(ValueError, match="status must be"):
         rmm.KV4Cache(*planes, status=rmm.status_word("cpu"))
+
+
+def test_scales_and_flags_of_numpy_types():
+    q, k = randn(4, 2, 64), randn(4, 1, 64)
+    cache = rmm.KV4Cache.empty(4, 1, 8, 64)
+    rmm.kv4_store(cache, k, k, i32([0] * 4))
+    lse = rmm.attn_prompt(q, k, k, scale=0.25, causal=True)[1]
+    for call in (lambda s, c: rmm.attn_prompt(q, k, k, scale=s, causal=c)[0],
+                 lambda s, c: rmm.attn_key_weights(q, k, lse, scale=s, causal=c),
+                 lambda s, c: rmm.kv4_attn(q, cache, i32([1] * 4), scale=s)[0]):
+        assert torch.equal(call(np.float32(0.25), np.bool_(True)), call(0.25, True))
+
+
+# ---------------------------------------------------------------- graphs
+def test_the_reduced_products_in_a_captured_graph():
+    """The fused calls of every route, captured once and replayed on other inputs."""
+    A, B = randn(96, 512, seed=1), randn(512, 256, seed=2)
+    x, n = randn(1, 512, seed=3), rmm.b_norms(B)
+    L, V = randn(2, 64, 128, seed=4), randn(2, 128, 64, seed=5)
+
+    def calls(outs, ws):
+        c0, w0 = rmm.matmul_reduced(A, B, 0.5, out=outs[0], workspace=ws[0])
+        c1, w1 = rmm.matmul_reduced_b_norms(x, B, n, 0.5, out=outs[1], workspace=ws[1])
+        c2, _, w2 = rmm.pv_softmax_reduced(L, V, 0.5, out=outs[2], P=outs[3], workspace=ws[2])
+        return [c0, c1, c2, _], [w0, w1, w2]
+
+    outs, ws = calls([None] * 4, [None] * 3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        calls(outs, ws)
+    for seed in (11, 12):
+        A.copy_(randn(96, 512, seed=seed))
+        x.copy_(randn(1, 512, seed=seed + 20))
+        L.copy_(randn(2, 64, 128, seed=seed + 40))
+        g.replay()
+        got = [t.clone() for t in outs]
+        for w in ws:
+            rmm.check(w)
+        want, _ = calls([None] * 4, [None] * 3)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
