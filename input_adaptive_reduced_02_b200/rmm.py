@@ -147,7 +147,10 @@ def _out_code(dt: torch.dtype) -> int:
 
 def _stream(t: torch.Tensor) -> int:
     """The handle of the current stream of t's device (a small call's time is the host's, so no Stream object is made)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    device = t.get_device()
+    if device < 0:  # which the lookup would take for the current device
+        raise ValueError("expected a CUDA tensor")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _ptr(t):

@@ -52,3 +52,12 @@ def test_status_words_and_workspaces_of_another_device_are_refused():
     assert rmm._ensure_ws(ws, 64, here) is ws and rmm._ensure_ws(ws, 65, here) is not ws
     with pytest.raises(ValueError, match="workspace is on"):
         rmm._ensure_ws(ws, 64, there)
+
+
+def test_host_tensors_never_reach_a_kernel():
+    """The softmax calls' logits are not looked at before the stream is asked for: a tensor of no device has none."""
+    L, V = torch.zeros(1, 8, 8), torch.zeros(1, 8, 16, dtype=torch.bfloat16)
+    for call in (lambda: rmm.softmax_row_stats(L), lambda: rmm.softmax_score(L, torch.zeros(1, 8, 2)),
+                 lambda: rmm.pv_softmax_reduced(L, V, 0.5)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
