@@ -951,13 +951,23 @@ cudaError_t launch_weights(TcArgs p, cudaStream_t st, const char** why) {
   const int64_t span = 2 * kRows;
   const int64_t units = (a.n_seq == 1 ? (a.T_k + span - 1) / span : a.T_k / span + a.n_seq) * a.h_kv;
   // Enough CTAs to even out the units' different lengths over 148 SMs, but at
-  // least 4 query tiles each. Beyond that a cluster costs more than it evens
-  // out: its CTAs need that many free SMs of one GPC at once (256 units of one
-  // prompt of 8192 tokens: 369, 363, 399 us alone, in pairs, in fours; 304
-  // units of a packed batch: 178, 142, 190 us).
+  // least 4 query tiles each on average. The CTAs of a cluster need that many
+  // free SMs of one GPC at once, so larger clusters pay only while all CTAs
+  // find room: eight while they fit the SMs, four up to about two per SM, pairs
+  // beyond (us alone, in pairs, fours, eights; d = 128):
+  //   16 units, 6 heads on one key head, 4096 tokens    307  160   90   51
+  //   32 units, 1024 tokens                              51   33   23   33
+  //   64 units, 2048 tokens                              96   57   45   66
+  //  128 units, 4096 tokens                             186  102  123  164
+  //  256 units, 8192 tokens                             363  346  404  506
+  //  312 units, a packed batch                          184  148  191  281
+  //  512 units, 16384 tokens                           1278 1255 1454 1761
+  // (d = 64: 128 units 33, 29, 43, 78; 256 units 57, 72, 102, 172.)
   const int64_t q_tiles = (a.T_q / std::max<int64_t>(a.n_seq, 1)) / p.nq_tile;
   p.split = 1;
-  while (p.split < 8 && units * p.split < 400 && q_tiles >= 8 * int64_t(p.split)) p.split *= 2;
+  if (units < 400 && q_tiles >= 8) p.split = 2;
+  if (units * 4 <= 320 && q_tiles >= 16) p.split = 4;
+  if (units * 8 <= 148 && q_tiles >= 32) p.split = 8;
   return launch_pdl(attn_key_weights_kernel<DP>, dim3(unsigned(units * p.split)), dim3(kWtThreads), Cfg::SMEM, st,
                     p.split > 1 ? dim3(p.split, 1, 1) : dim3(0, 0, 0), tmQ, tmK, p);
 }
