@@ -465,7 +465,8 @@ rmm_status rmm_matmul_reduced_noalloc(const void* A, int64_t lda, const void* B,
  * Packed sequences: sequence i's tokens are [cu[i], cu[i+1]), cu a device
  * array of n_seq + 1 ascending int32; NULL for a single sequence of all
  * tokens. Boundaries are clamped to the token count on the device; tokens of
- * no sequence are neither read as keys nor written. */
+ * no sequence are neither read as keys nor written. Outputs must not overlap
+ * inputs or one another unless a call says so. */
 
 /* O = softmax(scale·Q·Kᵀ)·V per sequence and head.
  *   Q [T_q][h_q][d], K, V [T_k][h_kv][d], O [T_q][h_q][d]: 16-byte aligned,
@@ -539,7 +540,8 @@ size_t rmm_kv4_attn_workspace_size(int64_t batch, int64_t h_q, int64_t h_kv, int
  * Workspace 1 KiB-aligned, its first word the status word (rmm_check), cleared
  * at the start; RMM_STATUS_BIT_NONFINITE: a head's sum is not a positive finite
  * number. Slots at and past lens[b] are not used. Queries beyond 2^100 may
- * overflow (infinite or NaN results); a probability times step 2^-26 or more
+ * overflow (infinite or NaN results), and a query channel 2^-28 or more below its
+ * head's largest loses bits of its own; a probability times step 2^-26 or more
  * below its query head's largest in the sequence loses bits of its own (what it
  * is rounded off by stays below 2^-37 of that largest product). */
 rmm_status rmm_kv4_attn(const void* Q, int64_t q_ss, int64_t q_hs, const uint8_t* kc, const void* ks,
@@ -615,7 +617,8 @@ uint64_t rmm_launch_count(void);
  *     check on the device that every kept index lies in [0, K), synchronise
  *     the stream, and return RMM_ERR_INVALID (naming the first bad entry)
  *     without launching the kernels that would read through a bad index;
- *   - the fused calls synchronise the stream after their kernels and return
+ *   - the fused calls, rmm_kv4_attn and rmm_cache_evict synchronise the stream
+ *     after their kernels and return
  *     RMM_ERR_NONFINITE / RMM_ERR_TIMEOUT from the status word directly (the
  *     word is left set for rmm_check).
  * Calls with debug checks on share one device word for the index check and

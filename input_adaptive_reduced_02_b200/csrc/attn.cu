@@ -963,6 +963,10 @@ cudaError_t launch_weights(TcArgs p, cudaStream_t st, const char** why) {
   //  312 units, a packed batch                          184  148  191  281
   //  512 units, 16384 tokens                           1278 1255 1454 1761
   // (d = 64: 128 units 33, 29, 43, 78; 256 units 57, 72, 102, 172.)
+  // The lengths are on the device, so the number of query tiles is an average.
+  // Batches of short prompts lose by clusters (16 x 256 tokens, 256 units: 25,
+  // 35; 64 x 32 tokens, 576 units: 29, 59); one long prompt among 31 short ones,
+  // which the average takes for short, would gain (184, 127).
   const int64_t q_tiles = (a.T_q / std::max<int64_t>(a.n_seq, 1)) / p.nq_tile;
   p.split = 1;
   if (units < 400 && q_tiles >= 8) p.split = 2;

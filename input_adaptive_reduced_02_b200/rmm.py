@@ -701,7 +701,8 @@ def attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.T
     Q [T_q][h_q][d], K, V [T_k][h_kv][d] bf16; sequence i's tokens are
     [cu[i], cu[i+1]) (int32, on the device; None: one sequence). With causal,
     query q sees key k when k <= q + S_k - S_q. scale defaults to 1/sqrt(d).
-    O [T_q][h_q][d]; lse f32 [h_q][T_q]."""
+    O [T_q][h_q][d]; lse f32 [h_q][T_q]. The probabilities are rounded to bf16
+    before they multiply V, whatever O's dtype (f32 sums, unrounded row sums)."""
     T_q, T_k, h_q, h_kv, d, q_ts, q_hs, k_ts, k_hs, n = _packed(Q, K, cu_q, cu_k)
     tv, hv, dv, v_ts, v_hs = _tokens(V, "V")
     device = Q.device
