@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from input_adaptive_reduced_02_b200 import rmm
-from test_attention_abi_cpu import DECODE, EVICT, P, PROMPT, STORE, UNSUPPORTED, WEIGHTS, call
+from test_attention_abi_cpu import DECODE, EVICT, PROMPT, STORE, UNSUPPORTED, WEIGHTS, call
 
 WIDE = dict(d=8, q_ts=65535 * 8, q_hs=8, k_ts=65535 * 8, k_hs=8, h_q=65535, h_kv=65535, n_seq=65535)
 
